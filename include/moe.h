@@ -229,6 +229,31 @@ moe_status moe_layer_forward(const moe_config* cfg, int64_t n, const void* x, co
                              moe_diag* diag_opt, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
+ * Whole layer for the few tokens of a decode step, in one kernel launch:
+ * n <= MOE_DECODE_MAX_TOKENS, otherwise MOE_ERR_UNSUPPORTED. Arguments and
+ * outputs are those of moe_layer_forward, every dtype and scoring; a capacity
+ * is a property of a large batch and cfg->cap_policy must be MOE_CAP_NONE
+ * (MOE_ERR_UNSUPPORTED otherwise).
+ *   x_codes_opt [n, d], x_scale_bytes_opt [n, d / 128]: MOE_FP8 only, both or
+ *   neither: the E4M3 tiles of x when the caller has them (moe_add_rmsnorm,
+ *   moe_quantize_fp8); NULL: the call quantises x. The router always reads x.
+ * Arithmetic: router logits are binary64 sums of exact products, so the
+ * indices are those of the binary64 definition with no second pass (diag's
+ * refined_* stay 0); expert products accumulate in binary32; the intermediate
+ * is rounded to the activation type (then to E4M3 for MOE_FP8) as in
+ * moe_expert_ffn; expert outputs stay binary32 and are rounded once, as y.
+ * The results differ from moe_layer_forward's by those roundings.
+ * ws: moe_workspace_size() bytes; two calls that overlap on the GPU need two
+ * workspaces (graphs replayed at once too). Waits between the launch's own
+ * blocks are bounded (2 s, then MOE_ERR_TIMEOUT in the status word).
+ */
+#define MOE_DECODE_MAX_TOKENS 64
+moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, const uint8_t* x_codes_opt,
+                            const uint8_t* x_scale_bytes_opt, const moe_weights* weights, void* y,
+                            int32_t* topk_idx_opt, float* topk_w_opt, int32_t* counts_opt, moe_diag* diag_opt,
+                            void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
  * E4M3 quantisation of bf16 rows in 1 x 128 tiles, the activation format of
  * the MOE_FP8 experts ([DS] FP8 section): for row r and tile t,
  * e = the smallest integer with max|x[r, 128t .. 128t+127]| <= 448 * 2^e
@@ -240,6 +265,31 @@ moe_status moe_layer_forward(const moe_config* cfg, int64_t n, const void* x, co
  */
 moe_status moe_quantize_fp8(const void* x, int64_t rows, int32_t cols, uint8_t* codes, uint8_t* scale_bytes,
                             moe_stream_t stream);
+
+/*
+ * Residual addition, root-mean-square norm and FP8 output: the step of a
+ * transformer block in front of the layer. The pages name the norm and the
+ * residual stream without a formula; per row, in binary32:
+ *   s = x + residual (s = x without one),   sum_out = s rounded to dtype,
+ *   y = s * weight / sqrt(mean(s^2) + eps), rounded once to dtype,
+ *   codes, scale_bytes = what moe_quantize_fp8 gives for y (for MOE_F32, the
+ *   same tiles of the binary32 y).
+ *   in : x [rows, cols], residual [rows, cols] or NULL, weight [cols] or NULL
+ *        (= 1), all of `dtype` (MOE_F32 or MOE_BF16); eps > 0.
+ *   out: sum_out [rows, cols] or NULL, y [rows, cols] or NULL, both of `dtype`;
+ *        codes [rows, cols] and scale_bytes [rows, cols / 128] (dense bytes),
+ *        both or neither. At least one of y and codes is given.
+ * The strides count elements from one row to the next (at least cols, rows
+ * 16-byte aligned; ignored for NULL). cols is a multiple of 8 (of 128 with
+ * codes) up to 32768. sum_out and y may each be x or residual themselves, with
+ * the same stride; any other overlap of an output is undefined. A row of zeros
+ * gives zeros. No workspace. MOE_ERR_INVALID_ARG for bad pointers, strides or
+ * sizes, MOE_ERR_UNSUPPORTED for cols that no kernel takes.
+ */
+moe_status moe_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                           const void* weight, float eps, int64_t rows, int32_t cols, int32_t dtype, void* sum_out,
+                           int64_t sum_stride, void* y, int64_t y_stride, uint8_t* codes, uint8_t* scale_bytes,
+                           moe_stream_t stream);
 
 /*
  * Hash routing ([DS4]): the experts of token t are row token_ids[t] of the

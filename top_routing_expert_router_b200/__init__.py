@@ -28,10 +28,11 @@ MOE_F32, MOE_BF16, MOE_FP8 = 0, 1, 2
 
 # Every symbol declared in include/moe.h.
 EXPORTS = ("moe_workspace_size", "moe_route", "moe_route_hash", "moe_bias_update", "moe_permute", "moe_expert_ffn",
-           "moe_combine", "moe_layer_forward", "moe_route_static_scratch", "moe_quantize_fp8",
-           "moe_ep_workspace_size", "moe_ep_layer_forward", "moe_ep_export_handle", "moe_ep_open_handle",
+           "moe_combine", "moe_layer_forward", "moe_layer_decode", "moe_route_static_scratch", "moe_quantize_fp8",
+           "moe_add_rmsnorm", "moe_ep_workspace_size", "moe_ep_layer_forward", "moe_ep_export_handle", "moe_ep_open_handle",
            "moe_ep_close_handle", "moe_sync_status", "moe_status_string")
 MOE_STATIC_SCRATCH_BYTES = 8 << 20  # include/moe.h
+MOE_DECODE_MAX_TOKENS = 64
 MOE_EP_MAX_RANKS = 8
 MOE_EP_HANDLE_BYTES = 72
 
@@ -80,10 +81,13 @@ _lib.moe_permute.argtypes = [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
 _lib.moe_expert_ffn.argtypes = [_P, _I64, _P, _P, _P, _P, _P, _SZ, _P]
 _lib.moe_combine.argtypes = [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
 _lib.moe_layer_forward.argtypes = [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+_lib.moe_layer_decode.argtypes = [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
 _lib.moe_route_hash.argtypes = [_P, _I64, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _SZ, _P]
 _lib.moe_bias_update.argtypes = [_P, _P, _P, ctypes.c_float, _P]
 _lib.moe_route_static_scratch.argtypes = [_P, _I64, _P, _P, _P, _P, _P, _P, _P]
 _lib.moe_quantize_fp8.argtypes = [_P, _I64, ctypes.c_int32, _P, _P, _P]
+_lib.moe_add_rmsnorm.argtypes = [_P, _I64, _P, _I64, _P, ctypes.c_float, _I64, ctypes.c_int32, ctypes.c_int32, _P, _I64,
+                                 _P, _I64, _P, _P, _P]
 _lib.moe_ep_workspace_size.argtypes = [_P, ctypes.c_int32, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)]
 _lib.moe_ep_layer_forward.argtypes = [_P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P]
 _lib.moe_ep_export_handle.argtypes = [_P, _P]
@@ -201,11 +205,81 @@ def moe_layer_forward(cfg, n, x, weights, y, ws, topk_idx=None, topk_w=None, cou
                                   _stream(stream)), "moe_layer_forward")
 
 
+def moe_layer_decode(cfg, n, x, weights, y, ws, topk_idx=None, topk_w=None, counts=None, diag=None, x_codes=None,
+                     x_scale_bytes=None, stream=None):
+    """moe_layer_forward for n <= MOE_DECODE_MAX_TOKENS tokens in one launch; x_codes and x_scale_bytes are x's E4M3
+    tiles (MOE_FP8) when the caller has them. Every tensor is contiguous and on ws's device."""
+    where = "moe_layer_decode"
+    dev, d, slots = ws.device, cfg.d_model, 4 * n * cfg.top_k
+    row = n * d * (4 if cfg.dtype == MOE_F32 else 2)
+    for name, t, need in (("x", x, row), ("y", y, row), ("topk_idx", topk_idx, slots), ("topk_w", topk_w, slots),
+                          ("counts", counts, 4 * cfg.n_routed), ("diag", diag, 32), ("x_codes", x_codes, n * d),
+                          ("x_scale_bytes", x_scale_bytes, n * (d // 128)), ("ws", ws, 0)):
+        if t is None:
+            continue
+        if t.device != dev or dev.type != "cuda":
+            raise ValueError(f"{where}: every tensor must be on the same CUDA device")
+        if t.nbytes < need or not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous with at least {need} bytes")
+    _call_on(dev.index, _lib.moe_layer_decode, where, ctypes.byref(cfg), n, _ptr(x), _ptr(x_codes), _ptr(x_scale_bytes),
+             ctypes.byref(weights), _ptr(y), _ptr(topk_idx), _ptr(topk_w), _ptr(counts), _ptr(diag), ws.data_ptr(),
+             ws.nbytes, stream=stream)
+
+
 def moe_quantize_fp8(x, codes, scale_bytes, stream=None):
     """E4M3 codes and UE8M0 scale bytes of bf16 rows x [rows, cols] in 1 x 128 tiles."""
     rows, cols = x.shape
     _check(_lib.moe_quantize_fp8(_ptr(x), rows, cols, _ptr(codes), _ptr(scale_bytes), _stream(stream)),
            "moe_quantize_fp8")
+
+
+def _call_on(index, fn, where, *args, stream=None):
+    """fn(*args, stream) with device `index` current; the stream is the device's current one unless given."""
+    import torch
+
+    if torch.cuda.current_device() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+    if st != MOE_OK:
+        raise MoeError(st, where)
+
+
+def moe_add_rmsnorm(x, weight, eps, y=None, residual=None, sum_out=None, codes=None, scale_bytes=None, stream=None):
+    """s = x + residual; sum_out = s; y = s * weight / sqrt(mean(s^2) + eps) by rows; codes and scale_bytes are the
+    E4M3 tiles of y. x, residual, sum_out and y are [rows, cols] of one dtype (torch.float32 or torch.bfloat16) whose
+    rows may be strided; weight is [cols] or None; codes [rows, cols] and scale_bytes [rows, cols / 128] are dense
+    torch.uint8. Every tensor is on x's device."""
+    import torch
+
+    where = "moe_add_rmsnorm"
+    dt, dev, shape = x.dtype, x.device, x.shape
+    if len(shape) != 2 or dt not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{where}: x must be [rows, cols] of torch.float32 or torch.bfloat16")
+    rows, cols = shape
+    address, stride = [], []
+    for t in (x, residual, sum_out, y):
+        if t is None:
+            address.append(None)
+            stride.append(0)
+            continue
+        step = t.stride()
+        if t.dtype != dt or t.shape != shape or step[1] != 1:
+            raise ValueError(f"{where}: residual, sum_out and y must be like x, with unit column stride")
+        if t.device != dev:
+            raise ValueError(f"{where}: every tensor must be on the same CUDA device")
+        address.append(t.data_ptr())
+        stride.append(step[0] if rows > 1 else cols)  # the stride of a single row is arbitrary
+    for name, t, want, of in (("weight", weight, (cols,), dt), ("codes", codes, (rows, cols), torch.uint8),
+                              ("scale_bytes", scale_bytes, (rows, cols // 128), torch.uint8)):
+        if t is not None and (t.dtype != of or t.shape != want or not t.is_contiguous() or t.device != dev):
+            raise ValueError(f"{where}: {name} must be contiguous {list(want)} of {of} on x's device")
+    if dev.type != "cuda":
+        raise ValueError(f"{where}: every tensor must be on the same CUDA device")
+    _call_on(dev.index, _lib.moe_add_rmsnorm, where, address[0], stride[0], address[1], stride[1], _ptr(weight), eps, rows,
+             cols, MOE_F32 if dt == torch.float32 else MOE_BF16, address[2], stride[2], address[3], stride[3], _ptr(codes),
+             _ptr(scale_bytes), stream=stream)
 
 
 def moe_ep_recv_rows_bound(cfg, world, token_counts) -> int:

@@ -22,6 +22,7 @@ struct Plan {
   size_t diag, logits, rq, rc, ranking, capg, blk, idx, w, counts, offsets, perm, dest, xperm, h, eo, shh, sh, shoff, sched;
   size_t xq, sfx, hq, sfh, xsq, sfxs, hsq, sfhs;  // FP8 experts: E4M3 activations and their scale blocks
   size_t sfb, sfbs;  // FP8 SM-pair GEMMs: B scale blocks (routed, shared experts)
+  size_t dctr, dlog, deo, des, dhs, dhss, dxs;  // moe_layer_decode: counters, binary64 logits, binary32 expert outputs, scale bytes
   size_t ep_off;  // expert parallelism: receive offsets of the rank's own experts
   size_t total;
   bool batched;   // the two-kernel router queues its undecided tokens for launch_refine (rq, rc reserved)
@@ -99,6 +100,9 @@ Plan make_plan(const moe_config& c, int64_t n, int32_t ep_world = 0, int64_t ep_
     return at;
   };
   p.diag = take(sizeof(moe_diag));
+  // the counters right behind the status word: one memset clears both
+  const bool few = !ep && n > 0 && n <= MOE_DECODE_MAX_TOKENS && c.cap_policy == MOE_CAP_NONE;
+  p.dctr = take(few ? (size_t)decode_counters(c.n_routed, c.d_model) * 4 : 0);
   p.logits = take((size_t)router_splits(c, n) * n * logits_ld(c) * 4);
   // the queue of tokens left to the binary64 router (one-pass router, or the first pass of the
   // two-kernel router), and their candidate experts: four counters, the candidate table, its
@@ -143,6 +147,12 @@ Plan make_plan(const moe_config& c, int64_t n, int32_t ep_world = 0, int64_t ep_
   p.sfb = take(fp8 ? sfb_bytes(fg, I, d) : 0);
   p.sfbs = take(fp8 && Is > 0 ? sfb_bytes(1, Is, d) : 0);
   p.ep_off = take(ep ? (size_t)(fg + 1) * 4 : 0);
+  p.dlog = take(few ? (size_t)n * c.n_routed * 8 : 0);
+  p.deo = take(few ? (size_t)nk * d * 4 : 0);
+  p.des = take(few && Is > 0 ? (size_t)n * d * 4 : 0);
+  p.dxs = take(few && fp8 ? (size_t)n * (d / 128) : 0);
+  p.dhs = take(few && fp8 ? (size_t)nk * (I / 128) : 0);
+  p.dhss = take(few && fp8 && Is > 0 ? (size_t)n * (Is / 128) : 0);
   p.total = off;
   return p;
 }
@@ -940,6 +950,78 @@ moe_status moe_layer_forward(const moe_config* cfg, int64_t n, const void* x, co
   return cuda_status(launch_combine(eo, dest, tw, sh, n, c.c.top_k, c.c.d_model, act_dtype(c.c), y, c.s));
 }
 
+moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, const uint8_t* x_codes_opt,
+                            const uint8_t* x_scale_bytes_opt, const moe_weights* weights, void* y,
+                            int32_t* topk_idx_opt, float* topk_w_opt, int32_t* counts_opt, moe_diag* diag_opt,
+                            void* ws, size_t ws_bytes, moe_stream_t stream) {
+  Ctx c;
+  MOE_TRY(begin(cfg, n, ws, ws_bytes, stream, &c));
+  if (cfg->cap_policy != MOE_CAP_NONE || n > MOE_DECODE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  if (!tok_ok(x, n) || !tok_ok(y, n) || !weights || !ptr_ok(weights->w_router)) return MOE_ERR_INVALID_ARG;
+  if ((topk_idx_opt && !tok_ok(topk_idx_opt, n)) || (topk_w_opt && !tok_ok(topk_w_opt, n)) ||
+      (counts_opt && !aligned(counts_opt, 4)) || (diag_opt && !aligned(diag_opt, 16)))
+    return MOE_ERR_INVALID_ARG;
+  const bool given = x_codes_opt || x_scale_bytes_opt;
+  if (given && (cfg->dtype != MOE_FP8 || !x_codes_opt || !x_scale_bytes_opt || !aligned(x_codes_opt, 16)))
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_weights(c.c, weights, true, true));
+  if (n == 0) {
+    MOE_TRY(clear_status(c));
+    if (diag_opt) MOE_CUDA(cudaMemsetAsync(diag_opt, 0, 5 * sizeof(int32_t), c.s));
+    if (counts_opt) MOE_CUDA(launch_fill_i32(counts_opt, c.c.n_routed, 0, c.s));
+    return MOE_OK;
+  }
+  const moe_config& f = c.c;
+  const bool fp8 = f.dtype == MOE_FP8;
+  DecodeArgs a{};
+  a.n = (int32_t)n;
+  a.d = f.d_model;
+  a.E = f.n_routed;
+  a.k = f.top_k;
+  a.G = f.n_group;
+  a.topk_group = f.topk_group;
+  a.score_fn = f.score_fn;
+  a.renorm = f.renormalize;
+  a.rsf = f.routed_scaling_factor;
+  a.I = f.moe_intermediate_size;
+  a.Is = f.n_shared * f.moe_intermediate_size;
+  a.dtype = f.dtype;
+  a.x = x;
+  a.w_router = weights->w_router;
+  a.bias = f.score_fn != MOE_SCORE_SOFTMAX ? weights->bias : nullptr;
+  a.w_gate = weights->w_gate;
+  a.w_up = weights->w_up;
+  a.w_down = weights->w_down;
+  a.ws_gate = weights->ws_gate;
+  a.ws_up = weights->ws_up;
+  a.ws_down = weights->ws_down;
+  a.s_gate = weights->w_gate_scale;
+  a.s_up = weights->w_up_scale;
+  a.s_down = weights->w_down_scale;
+  a.ss_gate = weights->ws_gate_scale;
+  a.ss_up = weights->ws_up_scale;
+  a.ss_down = weights->ws_down_scale;
+  a.quantize = fp8 && !given;
+  a.xq = given ? const_cast<uint8_t*>(x_codes_opt) : c.at<uint8_t>(c.p.xq);
+  a.xs = given ? const_cast<uint8_t*>(x_scale_bytes_opt) : c.at<uint8_t>(c.p.dxs);
+  a.logits = c.at<double>(c.p.dlog);
+  a.topk_idx = topk_idx_opt ? topk_idx_opt : c.at<int32_t>(c.p.idx);
+  a.topk_w = topk_w_opt ? topk_w_opt : c.at<float>(c.p.w);
+  a.h = fp8 ? c.at<void>(c.p.hq) : c.at<void>(c.p.h);
+  a.hs = fp8 ? c.at<void>(c.p.hsq) : c.at<void>(c.p.shh);
+  a.h_scale = c.at<uint8_t>(c.p.dhs);
+  a.hs_scale = c.at<uint8_t>(c.p.dhss);
+  a.eo = c.at<float>(c.p.deo);
+  a.es = c.at<float>(c.p.des);
+  a.y = y;
+  a.counts = counts_opt;
+  a.diag = diag_opt;
+  a.ctr = c.at<int32_t>(c.p.dctr);
+  a.status = c.status();
+  MOE_CUDA(cudaMemsetAsync(c.ws, 0, c.p.dctr + (size_t)decode_counters(a.E, a.d) * 4, c.s));
+  return cuda_status(launch_decode_simt(a, c.s));
+}
+
 moe_status moe_quantize_fp8(const void* x, int64_t rows, int32_t cols, uint8_t* codes, uint8_t* scale_bytes,
                             moe_stream_t stream) {
   if (rows < 0 || cols <= 0 || cols % 128 != 0 || rows * (int64_t)cols >= (int64_t)1 << 40) return MOE_ERR_INVALID_ARG;
@@ -947,6 +1029,35 @@ moe_status moe_quantize_fp8(const void* x, int64_t rows, int32_t cols, uint8_t* 
   if (!ptr_ok(x) || !ptr_ok(codes) || !scale_bytes) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_quantize_rows(x, nullptr, nullptr, 1, rows, cols, 128, codes, nullptr,
                                           reinterpret_cast<cudaStream_t>(stream), scale_bytes));
+}
+
+moe_status moe_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                           const void* weight, float eps, int64_t rows, int32_t cols, int32_t dtype, void* sum_out,
+                           int64_t sum_stride, void* y, int64_t y_stride, uint8_t* codes, uint8_t* scale_bytes,
+                           moe_stream_t stream) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || cols <= 0 || !(eps > 0.0f) || !isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  if ((!y && !codes) || (codes != nullptr) != (scale_bytes != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (codes && cols % 128 != 0) return MOE_ERR_INVALID_ARG;
+  if (cols % 8 != 0 || cols > kNormMaxCols) return MOE_ERR_UNSUPPORTED;
+  if (rows >= ((int64_t)1 << 40) / cols) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  const int64_t unit = dtype == MOE_BF16 ? 8 : 4;  // elements of 16 bytes
+  auto rows_ok = [&](const void* p, int64_t stride) {
+    return aligned(p, 16) && stride >= cols && stride % unit == 0 && stride < ((int64_t)1 << 40) / rows;
+  };
+  if (!x || !rows_ok(x, x_stride) || (residual && !rows_ok(residual, residual_stride)) ||
+      (sum_out && !rows_ok(sum_out, sum_stride)) || (y && !rows_ok(y, y_stride)) || !aligned(weight, 16) ||
+      !aligned(codes, 16))
+    return MOE_ERR_INVALID_ARG;
+  // an output in place shares its input's rows one to one, and the two outputs are apart
+  auto in_place_ok = [&](const void* o, int64_t os) {
+    return !o || ((o != x || os == x_stride) && (o != residual || os == residual_stride));
+  };
+  if (!in_place_ok(sum_out, sum_stride) || !in_place_ok(y, y_stride) || (y && y == sum_out)) return MOE_ERR_INVALID_ARG;
+  const NormArgs a{x,       x_stride,   residual, residual_stride, weight, eps,      rows,  cols,
+                   sum_out, sum_stride, y,        y_stride,        codes,  scale_bytes};
+  return cuda_status(launch_add_rmsnorm(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_ep_workspace_size(const moe_config* cfg, int32_t world, int64_t n, int64_t recv_rows, size_t* bytes) {

@@ -76,6 +76,27 @@ cudaError_t launch_quantize_rows(const void* src, const int32_t* src_row, const 
                                  int64_t rows_bound, int32_t cols, int32_t tile_rows, uint8_t* q, uint32_t* sf,
                                  cudaStream_t s, uint8_t* sf_plain = nullptr);
 
+// Residual addition, root-mean-square norm and E4M3 output (norm.cu). Row strides in elements,
+// 16-byte rows; residual, w, sum_out, y and (together) codes and scale_bytes may be null.
+constexpr int32_t kNormMaxCols = 32768;
+struct NormArgs {
+  const void* x;
+  int64_t x_stride;
+  const void* residual;
+  int64_t res_stride;
+  const void* w;
+  float eps;
+  int64_t rows;
+  int32_t cols;
+  void* sum_out;
+  int64_t sum_stride;
+  void* y;
+  int64_t y_stride;
+  uint8_t* codes;
+  uint8_t* scale_bytes;
+};
+cudaError_t launch_add_rmsnorm(const NormArgs& a, int dtype, cudaStream_t s);
+
 // Router: scoring, group limit, top-k, certification / binary64 refinement, gates.
 struct RouteArgs {
   const float* logits;  // [splits][n, ldl] partial logits (first E columns), summed in order
@@ -151,6 +172,37 @@ cudaError_t launch_route_tc(const RouteTcArgs& a, cudaStream_t s);
 // step of launch_route_tc on its own, for the tokens a deferring launch_route queued. Uses x, w_r,
 // d (bf16 rows, d % 8 == 0, 16-byte aligned), queue, cand, cand_val, pairs and pair_count.
 cudaError_t launch_refine(const RouteTcArgs& a, cudaStream_t s);
+
+// The whole layer for n <= MOE_DECODE_MAX_TOKENS tokens in one launch (decode.cuh has the scheme).
+// act: float (MOE_F32) or bf16; FP8 experts read x and h as E4M3 codes with UE8M0 bytes per 1 x 128.
+struct DecodeArgs {
+  int32_t n, d, E, k, G, topk_group, score_fn, renorm, I, Is, dtype;
+  float rsf;
+  const void* x;             // [n, d]
+  const void* w_router;      // [E, d]
+  const float* bias;         // [E] or nullptr
+  const void *w_gate, *w_up, *w_down, *ws_gate, *ws_up, *ws_down;
+  const uint8_t *s_gate, *s_up, *s_down, *ss_gate, *ss_up, *ss_down;
+  int32_t quantize;          // FP8: 1 = write xq, xs from x; 0 = they are given
+  uint8_t* xq;               // FP8: [n, d] codes
+  uint8_t* xs;               // FP8: [n, d / 128] scale bytes
+  double* logits;            // [n, E]
+  int32_t* topk_idx;         // [n, k]
+  float* topk_w;             // [n, k]
+  void* h;                   // [n * k, I] act, or E4M3 codes
+  void* hs;                  // [n, Is]
+  uint8_t* h_scale;          // FP8: [n * k, I / 128]
+  uint8_t* hs_scale;         // FP8: [n, Is / 128]
+  float* eo;                 // [n * k, d] expert outputs, rows by expert then token
+  float* es;                 // [n, d] shared experts' output
+  void* y;                   // [n, d]
+  int32_t* counts;           // [E] or nullptr
+  moe_diag* diag;            // or nullptr
+  int32_t* ctr;              // counters, zeroed before the launch
+  moe_diag* status;
+};
+int64_t decode_counters(int32_t E, int32_t d);  // counter words
+cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t s);
 
 // Capacity rule over the ranking on many SMs (capacity.cu): a cooperative grid, one token per
 // thread, one round per fill event. Needs capacity_grid_scratch_bytes of scratch (16-byte aligned)

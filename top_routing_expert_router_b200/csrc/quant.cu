@@ -12,35 +12,12 @@
 // scaling: the 32-bit word of tile row p sits at word 4 (p % 32) + p / 32, and
 // its byte j is the UE8M0 byte of column tile 4q + j (the GEMM's MMAs select the
 // byte of their k block).
-#include <cuda_fp8.h>
-
 #include "common.cuh"
+#include "fp8.cuh"
 #include "kernels.h"
 
 namespace moe {
 namespace {
-
-// UE8M0 exponent of a tile whose largest magnitude is amax (finite binary32):
-// with amax = f * 2^x, f in [0.5, 1), amax <= 448 * 2^e  <=>  f * 2^(x - 8 - e) <= 1.75,
-// so e = x - 9 when f <= 0.875 and x - 8 otherwise. For a normal amax = 1.m * 2^(E - 127)
-// that is x = E - 126 and f <= 0.875 <=> m <= 0.75, read straight off the bits.
-__device__ __forceinline__ int ue8m0_exponent(float amax) {
-  if (!(amax > 0.0f)) return 0;
-  const uint32_t u = __float_as_uint(amax);
-  const int E = (int)(u >> 23);
-  int e;
-  if (E > 0) {
-    e = (u & 0x7FFFFFu) <= 0x600000u ? E - 135 : E - 134;
-  } else {  // binary32 subnormal
-    int x;
-    const float f = frexpf(amax, &x);
-    e = f <= 0.875f ? x - 9 : x - 8;
-  }
-  return e < -127 ? -127 : (e > 127 ? 127 : e);
-}
-
-// 2^-e as a binary32 (normal for the exponents bf16 inputs produce, -127 <= e <= 119).
-__device__ __forceinline__ float pow2_neg(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
 
 constexpr int kQuantWarps = 8;
 
@@ -114,16 +91,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
         for (int off = 8; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(hmask, m, off));
         const int e = ue8m0_exponent(m);
         const float sc = pow2_neg(e);  // multiplying by 2^-e is exact for these magnitudes
-        uint32_t w[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const __nv_fp8x2_storage_t c01 = __nv_cvt_float2_to_fp8x2(
-              make_float2(v[4 * j] * sc, v[4 * j + 1] * sc), __NV_SATFINITE, __NV_E4M3);
-          const __nv_fp8x2_storage_t c23 = __nv_cvt_float2_to_fp8x2(
-              make_float2(v[4 * j + 2] * sc, v[4 * j + 3] * sc), __NV_SATFINITE, __NV_E4M3);
-          w[j] = (uint32_t)c01 | ((uint32_t)c23 << 16);
-        }
-        out[t * 16 + hl] = make_uint2(w[0], w[1]);
+        out[t * 16 + hl] = make_uint2(e4m3x4(v[0], v[1], v[2], v[3], sc), e4m3x4(v[4], v[5], v[6], v[7], sc));
         if (hl == 0) {
           const uint32_t byte = (uint32_t)(e + 127);
           if (sf_plain)
