@@ -1018,8 +1018,10 @@ moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, con
   a.diag = diag_opt;
   a.ctr = c.at<int32_t>(c.p.dctr);
   a.status = c.status();
+  const bool tensor = f.dtype != MOE_F32;
+  if (tensor && !decode_tc_supported(a)) return MOE_ERR_UNSUPPORTED;
   MOE_CUDA(cudaMemsetAsync(c.ws, 0, c.p.dctr + (size_t)decode_counters(a.E, a.d) * 4, c.s));
-  return cuda_status(launch_decode_simt(a, c.s));
+  return cuda_status(tensor ? launch_decode_tc(a, c.s) : launch_decode_simt(a, c.s));
 }
 
 moe_status moe_quantize_fp8(const void* x, int64_t rows, int32_t cols, uint8_t* codes, uint8_t* scale_bytes,

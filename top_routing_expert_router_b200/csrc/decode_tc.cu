@@ -1,0 +1,667 @@
+// decode_tc.cu -- the one-kernel layer for few tokens on the tcgen05 tensor cores (bf16 and FP8
+// experts; decode.cuh has the scheme and the router).
+//
+// The weights are the M side: a tile is two blocks of 128 weight rows (gate and up rows of the same
+// 128 hidden columns; 256 output columns of a down matrix) times N token columns, N = the tokens
+// rounded up to 16. D0 and D1, 128 x N binary32 each in TMEM, hold a token per column, so a gate/up
+// tile multiplies every token of the batch and stores the columns of the expert's tokens: no row is
+// gathered and no operand is padded to 128 rows. At N <= 64 the MMAs take under a tenth of the time
+// the weights take to arrive; the kernel is bound by HBM.
+//
+// One CTA per SM, 384 threads, warp-specialised:
+//   warp 0      claims tiles and copies their weights (TMA, 128-byte swizzle) into a ring of 32 KB
+//               stages, running ahead of everything else: at the turn from gate/up to down tiles the
+//               ring already holds down weights while other CTAs finish h.
+//   warp 2      copies the token operand of each stage (x, or h once its expert's gate/up tiles are
+//               finished) and, for FP8, writes the stage's scale words.
+//   warp 1      owns TMEM and issues the MMAs; tcgen05.commit frees stages.
+//   warps 4-7   router, then the epilogue: SwiGLU and h (FP8: its E4M3 tile, whose 128 columns are
+//               the tile's 128 lanes), or the down tile's rows and, after a column range's last
+//               tile, the combine.
+//   warps 8-11  router.
+// The shared experts' tiles need no routing and come first, so the weights stream while the router
+// runs. FP8 scales ride in the MMA (kind::mxf8f6f4.block_scale): one scale word holds four 128-wide
+// k blocks, so every fourth stage carries scale words, copied into TMEM by tcgen05.cp.
+#include <cuda.h>
+#include <limits.h>
+
+#include "decode.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 384;
+constexpr int kRouterWarps = 8, kRouterThreads = 32 * kRouterWarps;  // warps 4..11
+constexpr int kRows = 128;                  // weight rows of an MMA
+constexpr int kKB = 128;                    // bytes of k per stage and row
+constexpr int kABytes = kRows * kKB;        // one weight block
+constexpr int kSfBytes = 512;
+constexpr int kColumns = 2 * kRows;         // output columns of a down tile
+constexpr int kMaxStages = 8;
+constexpr int kQueue = 4;                   // tiles published ahead of the slowest reader
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSfCol0 = 256;           // after two pairs of accumulators of at most 64 columns
+constexpr uint32_t kSfCols = 12;            // per slot: D0's rows, D1's rows, the tokens
+constexpr size_t kSmemLimit = 232448;
+
+struct __align__(16) Ctl {
+  uint64_t full[kMaxStages];   // weights' and tokens' arrivals
+  uint64_t empty[kMaxStages];
+  uint64_t tmem_full[2];
+  uint64_t tmem_empty[2];
+  uint64_t tile_full[kQueue];
+  uint64_t tile_empty[kQueue];  // read by the MMA, the token producer and four epilogue warps
+  uint64_t plan_ready;
+  uint64_t drain;
+  int32_t tile[kQueue];
+  uint32_t tmem_base;
+  int32_t abort;
+  int32_t ticket;
+  int32_t routed;              // every token's decision was seen
+  int32_t last;
+  float4 amax[16];             // FP8: a column's largest |h| per epilogue warp
+  double part[kRouterWarps * kRouterTokens];
+  DecideScratch decide;
+  DecodePlan plan;
+};
+
+struct DecodeMaps {
+  CUtensorMap gate, up, down, sgate, sup, sdown, x, h, hs;
+};
+
+struct TcShape {
+  int32_t n_cols;       // token columns: n rounded up to 16
+  int32_t stages;
+  int32_t stage_bytes;
+  int32_t slot_off;     // bytes from the ring to the combine's slots
+  int32_t ctl_off;
+};
+
+__device__ __noinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* ctr, moe_diag* st) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try(b, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try(b, parity)) return true;
+    if ((it & 255u) == 0) {
+      if (*reinterpret_cast<volatile int32_t*>(&ctl->abort)) return false;
+      if (globaltimer() - t0 > kDecodeTimeoutNs) {
+        atomicExch(&ctl->abort, 1);
+        atomicExch(ctr + kCtrAbort, 1);
+        set_status(st, MOE_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+// kind::f16 (bf16 A and B) and kind::mxf8f6f4 (E4M3, UE8M0 scales; scale byte `id` of the words)
+// instruction descriptors: binary32 D, K-major operands, M = 128, N = n.
+__device__ __forceinline__ uint32_t idesc_bf16(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t idesc_fp8(int n, int id) {
+  return ((uint32_t)id << 4) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(kRows >> 4) << 24) |
+         ((uint32_t)id << 29);
+}
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+__device__ __forceinline__ void sf_copy(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Orders generic writes before, and async-proxy (TMA) reads after, across the release/acquire pair between them.
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+template <int ID, int COUNT>
+__device__ __forceinline__ void named_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(COUNT) : "memory");
+}
+
+// Barrier of COUNT threads that tells each whether all of them came with `v`.
+template <int ID, int COUNT>
+__device__ __forceinline__ bool named_and(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "n"(ID), "n"(COUNT)
+      : "memory");
+  return r != 0;
+}
+
+// A tile's place in the layer.
+struct Tile {
+  int e;        // expert, or E for the shared ones
+  int r0;       // first weight row (down: output column) of the tile
+  int down;
+  int Ie;       // hidden width of the expert
+  int row0, m;  // its token rows: slots row0 .. row0 + m (shared: every token)
+  unsigned long long mask;
+};
+
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_constant__ DecodeMaps maps,
+                                                               const __grid_constant__ DecodeArgs a,
+                                                               const __grid_constant__ TcShape sh) {
+  constexpr int KE = FP8 ? 128 : 64;  // elements of k per stage
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + sh.ctl_off);
+  float* slot_w = reinterpret_cast<float*>(smem + sh.slot_off);           // [n * k] gates
+  uint16_t* slot_r = reinterpret_cast<uint16_t*>(slot_w + a.n * a.k);     // [n * k] expert output rows (0xFFFF: none)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int N = sh.n_cols, stages = sh.stages;
+  const int shared = a.Is > 0;
+  const int tiles1 = (a.I + kRows - 1) / kRows, tiles1s = (a.Is + kRows - 1) / kRows;
+  const int tiles2 = (a.d + kColumns - 1) / kColumns;
+
+  if (threadIdx.x == 0) {
+    ctl->abort = 0;
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&ctl->full[s], 2);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctl->tmem_full[b], 1);
+      mbar_init(&ctl->tmem_empty[b], 4);
+    }
+    for (int q = 0; q < kQueue; ++q) {
+      mbar_init(&ctl->tile_full[q], 1);
+      mbar_init(&ctl->tile_empty[q], 6);
+    }
+    mbar_init(&ctl->plan_ready, kRouterWarps);
+    mbar_init(&ctl->drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem_base = ctl->tmem_base;
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_try(smem_u32(bar), parity) || mbar_wait(bar, parity, ctl, a.ctr, a.status);
+  };
+  auto tile_of = [&](int t) {
+    Tile tl;
+    const int first2 = t < tiles1s ? INT_MAX : tiles1s + ctl->plan.n_act * tiles1;  // the plan is ready past the first tiles
+    tl.down = t >= first2;
+    int u;
+    if (tl.down) {
+      u = (t - first2) / tiles2 - shared;
+      tl.r0 = (t - first2) % tiles2 * kColumns;
+    } else {
+      u = t < tiles1s ? -1 : (t - tiles1s) / tiles1;
+      tl.r0 = (u < 0 ? t : (t - tiles1s) % tiles1) * kRows;
+    }
+    tl.e = u < 0 ? a.E : ctl->plan.act[u];
+    tl.Ie = u < 0 ? a.Is : a.I;
+    tl.mask = u < 0 ? token_mask(a.n) : ctl->plan.mask[tl.e];
+    tl.row0 = u < 0 ? 0 : ctl->plan.off[tl.e];
+    tl.m = __popcll(tl.mask);
+    return tl;
+  };
+  // Stages of a tile, and whether its second weight block has any row.
+  auto k_blocks = [&](const Tile& tl) { return ((tl.down ? tl.Ie : a.d) + KE - 1) / KE; };
+  auto two_blocks = [&](const Tile& tl) { return !tl.down || tl.r0 + kRows < a.d; };
+  // Token columns of a tile: all of them, or a routed down tile's own rows.
+  auto columns = [&](const Tile& tl) { return tl.down && tl.e < a.E ? (tl.m + 15) & ~15 : N; };
+
+  if (warp == 0) {
+    // ================= weights =================
+    if (lane == 0) {
+      int stage = 0, q = 0;
+      uint32_t phase = 0, qphase = 0, armed = 0;
+      bool ok = true;
+      int total = INT_MAX, next = atomicAdd(a.ctr + kCtrTile, 1);
+      while (ok) {
+        const int t = next;
+        if (t >= tiles1s && total == INT_MAX) {
+          if (!(ok = wait(&ctl->plan_ready, 0))) break;
+          total = tiles1s + ctl->plan.n_act * tiles1 + (ctl->plan.n_act + shared) * tiles2;
+        }
+        if (!(ok = wait(&ctl->tile_empty[q], qphase ^ 1u))) break;
+        ctl->tile[q] = t < total ? t : -1;
+        mbar_arrive(&ctl->tile_full[q]);
+        if (++q == kQueue) q = 0, qphase ^= 1u;
+        if (t >= total) break;
+        next = atomicAdd(a.ctr + kCtrTile, 1);
+        const Tile tl = tile_of(t);
+        const bool s = tl.e == a.E, two = two_blocks(tl);
+        const CUtensorMap* m0 = tl.down ? (s ? &maps.sdown : &maps.down) : (s ? &maps.sgate : &maps.gate);
+        const CUtensorMap* m1 = tl.down ? m0 : (s ? &maps.sup : &maps.up);
+        const int y0 = (s ? 0 : tl.e * (tl.down ? a.d : a.I)) + tl.r0, y1 = tl.down ? y0 + kRows : y0;
+        const int nkb = k_blocks(tl);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!(ok = wait(&ctl->empty[stage], phase ^ 1u))) break;
+          uint8_t* sa = smem + stage * sh.stage_bytes;
+          mbar_expect_tx(&ctl->full[stage], two ? 2 * kABytes : kABytes);
+          tma_load_2d(sa, m0, &ctl->full[stage], kb * KE, y0);
+          if (two) tma_load_2d(sa + kABytes, m1, &ctl->full[stage], kb * KE, y1);
+          ++armed;
+          if (++stage == stages) stage = 0, phase ^= 1u;
+        }
+      }
+      if (!ok)  // let the copies in flight land
+        for (uint32_t s = 0; s < (uint32_t)stages; ++s)
+          if (armed > s) mbar_drain(&ctl->full[s], ((armed - 1 - s) / stages) & 1u);
+    }
+  } else if (warp == 1) {
+    // ================= MMA =================
+    if (lane == 0) {
+      int stage = 0, q = 0, i = 0;
+      uint32_t phase = 0, qphase = 0;
+      bool ok = true, issued = false;
+      for (;; ++i) {
+        if (!(ok = wait(&ctl->tile_full[q], qphase))) break;
+        const int t = ctl->tile[q];
+        if (t < 0) break;
+        const Tile tl = tile_of(t);
+        mbar_arrive(&ctl->tile_empty[q]);
+        if (++q == kQueue) q = 0, qphase ^= 1u;
+        const int buf = i & 1;
+        if (!(ok = wait(&ctl->tmem_empty[buf], ((uint32_t)(i >> 1) & 1u) ^ 1u))) break;
+        fence_after();
+        const uint32_t d0 = tmem_base + (uint32_t)(buf * 2 * N), d1 = d0 + (uint32_t)N;
+        const bool two = two_blocks(tl);
+        const int nkb = k_blocks(tl), cols = columns(tl);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!(ok = wait(&ctl->full[stage], phase))) break;
+          fence_after();
+          const uint32_t sa = smem_u32(smem + stage * sh.stage_bytes);
+          const uint64_t a0 = sw128_desc(sa), a1 = sw128_desc(sa + kABytes), b = sw128_desc(sa + 2 * kABytes);
+          if constexpr (FP8) {
+            const uint32_t sf = tmem_base + kSfCol0 + kSfCols * (uint32_t)((kb >> 2) & 1);
+            if ((kb & 3) == 0) {
+              const uint32_t ss = sa + 2 * kABytes + (uint32_t)N * kKB;
+              sf_copy(sf, sf_desc(ss));
+              sf_copy(sf + 4, sf_desc(ss + kSfBytes));
+              sf_copy(sf + 8, sf_desc(ss + 2 * kSfBytes));
+            }
+            const uint32_t id = idesc_fp8(cols, kb & 3);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // 32 codes = 32 bytes
+              mma_fp8(d0, a0 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, sf, sf + 8, (kb | k) != 0);
+              if (two) mma_fp8(d1, a1 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, sf + 4, sf + 8, (kb | k) != 0);
+            }
+          } else {
+            const uint32_t id = idesc_bf16(cols);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // 16 bf16 = 32 bytes
+              mma_bf16(d0, a0 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, (kb | k) != 0);
+              if (two) mma_bf16(d1, a1 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, (kb | k) != 0);
+            }
+          }
+          issued = true;
+          mma_commit(&ctl->empty[stage]);
+          if (++stage == stages) stage = 0, phase ^= 1u;
+        }
+        if (!ok) break;
+        mma_commit(&ctl->tmem_full[buf]);
+      }
+      if (!ok && issued) {
+        mma_commit(&ctl->drain);
+        mbar_drain(&ctl->drain, 0);
+      }
+    }
+  } else if (warp == 2) {
+    // ================= tokens (and FP8 scale words) =================
+    int stage = 0, q = 0;
+    uint32_t phase = 0, qphase = 0;
+    bool quant_ok = !(FP8 && a.quantize);
+    const int quants = (a.n * (a.d / 128) + kRouterWarps - 1) / kRouterWarps;
+    auto all = [&](bool v) { return __shfl_sync(kFull, (int)v, 0) != 0; };
+    for (;;) {
+      if (!all(lane != 0 || wait(&ctl->tile_full[q], qphase))) break;
+      __syncwarp();
+      const int t = *reinterpret_cast<volatile int32_t*>(&ctl->tile[q]);
+      if (t < 0) break;
+      const Tile tl = tile_of(t);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->tile_empty[q]);
+      if (++q == kQueue) q = 0, qphase ^= 1u;
+      // what this tile reads is written: x's codes, or h of its expert
+      bool ok = true;
+      if (lane == 0) {
+        if (tl.down)
+          ok = wait_counter(a.ctr + kCtrExpert + tl.e, tl.e == a.E ? tiles1s : tiles1, a.ctr, a.status);
+        else if (!quant_ok)
+          ok = wait_counter(a.ctr + kCtrQuantDone, quants, a.ctr, a.status);
+        fence_async_global();
+        if (!ok) atomicExch(&ctl->abort, 1);
+      }
+      if (!all(ok)) break;
+      quant_ok = true;
+      const bool s = tl.e == a.E;
+      const CUtensorMap* m = !tl.down ? &maps.x : (s ? &maps.hs : &maps.h);
+      const int cols = columns(tl), nkb = k_blocks(tl);
+      // scale bytes: rows of the token operand, and the two weight blocks
+      const uint8_t *tok = nullptr, *w0 = nullptr, *w1 = nullptr;
+      if constexpr (FP8) {
+        if (tl.down) {
+          tok = s ? a.hs_scale : a.h_scale + (int64_t)tl.row0 * nkb;
+          w0 = (s ? a.ss_down : a.s_down + (int64_t)tl.e * (a.d / 128) * nkb) + (int64_t)(tl.r0 / 128) * nkb;
+          w1 = two_blocks(tl) ? w0 + nkb : w0;
+        } else {
+          tok = a.xs;
+          const int64_t at = (s ? 0 : (int64_t)tl.e * (a.I / 128) * nkb) + (int64_t)(tl.r0 / 128) * nkb;
+          w0 = (s ? a.ss_gate : a.s_gate) + at;
+          w1 = (s ? a.ss_up : a.s_up) + at;
+        }
+      }
+      const int rows = tl.down && !s ? tl.m : a.n;
+      auto word = [&](const uint8_t* p, int kb, bool own) {  // scale bytes of k blocks kb .. kb + 3
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (kb + j < nkb) w |= (uint32_t)(own ? __ldcg(p + kb + j) : __ldg(p + kb + j)) << (8 * j);
+        return w;
+      };
+      uint32_t wt0 = 0, wt1 = 0, ww0 = 0, ww1 = 0;
+      auto fetch = [&](int kb) {  // lane l holds token rows l and l + 32
+        if (kb >= nkb) return;
+        wt0 = lane < rows ? word(tok + (int64_t)lane * nkb, kb, true) : 0u;
+        wt1 = lane + 32 < rows ? word(tok + (int64_t)(lane + 32) * nkb, kb, true) : 0u;
+        ww0 = word(w0, kb, false);
+        ww1 = word(w1, kb, false);
+      };
+      if constexpr (FP8) fetch(0);
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!all(lane != 0 || wait(&ctl->empty[stage], phase ^ 1u))) {
+          ok = false;
+          break;
+        }
+        uint8_t* sb = smem + stage * sh.stage_bytes + 2 * kABytes;
+        if (FP8 && (kb & 3) == 0) {
+          uint4* sf = reinterpret_cast<uint4*>(sb + N * kKB);
+          sf[lane] = make_uint4(ww0, ww0, ww0, ww0);
+          sf[32 + lane] = make_uint4(ww1, ww1, ww1, ww1);
+          sf[64 + lane] = make_uint4(wt0, wt1, 0u, 0u);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          fetch(kb + 4);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_expect_tx(&ctl->full[stage], (uint32_t)cols * kKB);
+          if (tl.down && !s)
+            for (int c = 0; c < cols; c += 16) tma_load_2d(sb + c * kKB, m, &ctl->full[stage], kb * KE, tl.row0 + c);
+          else
+            tma_load_2d(sb, m, &ctl->full[stage], kb * KE, 0);
+        }
+        if (++stage == stages) stage = 0, phase ^= 1u;
+      }
+      if (!ok) break;
+    }
+  } else if (warp >= 4) {
+    // ================= router =================
+    const int tid = threadIdx.x - 128, rw = warp - 4;
+    auto sync = [] { named_sync<1, kRouterThreads>(); };
+    const int quants = FP8 && a.quantize ? (a.n * (a.d / 128) + kRouterWarps - 1) / kRouterWarps : 0;
+    const int unit = router_unit(a.E, gridDim.x), units = (a.E + unit - 1) / unit;
+    for (;;) {  // E4M3 tiles of x, then logits
+      if (tid == 0) ctl->ticket = atomicAdd(a.ctr + kCtrLogit, 1);
+      sync();
+      const int u = ctl->ticket;
+      if (u >= quants + units) break;
+      if (u < quants) {
+        const int i = u * kRouterWarps + rw;
+        if (i < a.n * (a.d / 128)) quantize_x_tile(a, i);
+        fence_async_global();  // the codes are read by TMA
+      } else {
+        const int e0 = (u - quants) * unit;
+        router_logits_unit<bf16, kRouterWarps>(a, e0, min(a.E, e0 + unit), rw, ctl->part, sync);
+      }
+      __threadfence();
+      sync();
+      if (tid == 0) add_release(a.ctr + (u < quants ? kCtrQuantDone : kCtrLogitDone), 1);
+    }
+    bool ok = true;
+    if (rw == 0) {  // one warp a block decides tokens: there are more blocks than tokens
+      for (;;) {
+        int t = 0;
+        if (lane == 0) t = atomicAdd(a.ctr + kCtrToken, 1);
+        t = __shfl_sync(kFull, t, 0);
+        if (t >= a.n) break;
+        if (lane == 0) ok = wait_counter(a.ctr + kCtrLogitDone, units, a.ctr, a.status);
+        if (!(ok = __shfl_sync(kFull, (int)ok, 0) != 0)) break;
+        decide_token_any(a, t, &ctl->decide);
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) add_release(a.ctr + kCtrTokenDone, 1);
+      }
+      if (lane == 0) {
+        if (ok) ok = wait_counter(a.ctr + kCtrTokenDone, a.n, a.ctr, a.status);
+        if (!ok) atomicExch(&ctl->abort, 1);
+        ctl->routed = ok;
+      }
+    }
+    sync();
+    ok = ctl->routed != 0;  // one answer for all: the barriers below count every router warp
+    if (ok) {
+      build_plan<kRouterThreads>(a, &ctl->plan, tid, sync);
+      for (int s = tid; s < a.n * a.k; s += kRouterThreads) {
+        const int e = __ldcg(a.topk_idx + s);
+        slot_w[s] = __ldcg(a.topk_w + s);
+        slot_r[s] = e < 0 ? (uint16_t)0xFFFF : (uint16_t)slot_row(ctl->plan, e, s / a.k);
+      }
+      sync();
+      if (lane == 0) mbar_arrive(&ctl->plan_ready);
+      if (blockIdx.x == 0 && rw >= 4) write_counts<kRouterThreads - 128>(a, ctl->plan, tid - 128);
+    }
+    if (ok && rw < 4) {
+      // ================= epilogue (warps 4..7) =================
+      const int r = rw * 32 + lane;  // weight row of the tile: TMEM lane (quarter rw = warp % 4)
+      int q = 0, i = 0;
+      uint32_t qphase = 0;
+      for (;; ++i) {
+        const int buf = i & 1;
+        bool go = wait(&ctl->tile_full[q], qphase);
+        const int t = go ? *reinterpret_cast<volatile int32_t*>(&ctl->tile[q]) : 0;
+        if (go && t >= 0) go = wait(&ctl->tmem_full[buf], (uint32_t)(i >> 1) & 1u);
+        // one answer for the four warps: the barriers below count all of them
+        if (!named_and<2, 128>(go) || t < 0) break;
+        const Tile tl = tile_of(t);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->tile_empty[q]);
+        if (++q == kQueue) q = 0, qphase ^= 1u;
+        fence_after();
+        const uint32_t d0 = tmem_base + ((uint32_t)(rw * 32) << 16) + (uint32_t)(buf * 2 * N), d1 = d0 + (uint32_t)N;
+        const bool s = tl.e == a.E;
+        if (!tl.down) {
+          const int c = tl.r0 + r;  // hidden column
+          for (int t0 = 0; t0 < N; t0 += 16) {
+            const uint32_t mine = (uint32_t)(tl.mask >> t0) & 0xFFFFu;
+            if (!mine) continue;
+            float g[16], u[16];
+            tmem_ld16(d0 + (uint32_t)t0, g);
+            tmem_ld16(d1 + (uint32_t)t0, u);
+            int row = tl.row0 + __popcll(tl.mask & ((1ull << t0) - 1ull));
+            if constexpr (FP8) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (!((mine >> j) & 1u)) continue;
+                g[j] = to_f32(from_f32<bf16>(silu(g[j]) * u[j]));
+                const float v = fabsf(g[j]);  // a NaN is left out of the maximum
+                const unsigned top = __reduce_max_sync(kFull, v >= 0.0f ? __float_as_uint(v) : 0u);
+                if (lane == 0) reinterpret_cast<float*>(&ctl->amax[j])[rw] = __uint_as_float(top);
+              }
+              named_sync<2, 128>();
+              uint8_t* hq = static_cast<uint8_t*>(s ? a.hs : a.h);
+              uint8_t* hb = s ? a.hs_scale : a.h_scale;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (!((mine >> j) & 1u)) continue;
+                const float4 m4 = ctl->amax[j];
+                const int e = ue8m0_exponent(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)));
+                hq[(int64_t)row * tl.Ie + c] = (uint8_t)__nv_cvt_float_to_fp8(g[j] * pow2_neg(e), __NV_SATFINITE, __NV_E4M3);
+                if (r == 0) hb[(int64_t)row * (tl.Ie / 128) + tl.r0 / 128] = (uint8_t)(e + 127);
+                ++row;
+              }
+              named_sync<2, 128>();  // amax is the next columns'
+            } else {
+              bf16* h = static_cast<bf16*>(s ? a.hs : a.h);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (!((mine >> j) & 1u)) continue;
+                if (c < tl.Ie) h[(int64_t)row * tl.Ie + c] = from_f32<bf16>(silu(g[j]) * u[j]);
+                ++row;
+              }
+            }
+          }
+        } else {
+          float* out = s ? a.es : a.eo + (int64_t)tl.row0 * a.d;
+          const bool two = two_blocks(tl);
+          for (int t0 = 0; t0 < tl.m; t0 += 16) {
+            float v0[16], v1[16];
+            tmem_ld16(d0 + (uint32_t)t0, v0);
+            if (two) tmem_ld16(d1 + (uint32_t)t0, v1);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (t0 + j >= tl.m) break;
+              float* o = out + (int64_t)(t0 + j) * a.d + tl.r0 + r;
+              if (tl.r0 + r < a.d) o[0] = v0[j];
+              if (tl.r0 + kRows + r < a.d) o[kRows] = v1[j];
+            }
+          }
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->tmem_empty[buf]);
+        fence_async_global();  // h is read by TMA
+        __threadfence();
+        named_sync<2, 128>();
+        if (!tl.down) {
+          if (r == 0) add_release(a.ctr + kCtrExpert + tl.e, 1);
+          continue;
+        }
+        if (r == 0) ctl->last = add_release(a.ctr + kCtrExpert + a.E + 1 + tl.r0 / kColumns, 1) + 1 == ctl->plan.n_act + shared;
+        named_sync<2, 128>();
+        if (!ctl->last) continue;
+        // the last expert's tile of these columns adds them up, in slot order, the shared experts last
+        const int c = tl.r0 + 2 * r;
+        if (c < a.d) {
+          for (int t2 = 0; t2 < a.n; ++t2) {
+            float2 y = make_float2(0.0f, 0.0f);
+            for (int j = 0; j < a.k; ++j) {
+              const int row = slot_r[t2 * a.k + j];
+              if (row == 0xFFFF) continue;
+              const float w = slot_w[t2 * a.k + j];
+              const float2 o = __ldcg(reinterpret_cast<const float2*>(a.eo + (int64_t)row * a.d + c));
+              y.x = fmaf(w, o.x, y.x);
+              y.y = fmaf(w, o.y, y.y);
+            }
+            if (shared) {
+              const float2 o = __ldcg(reinterpret_cast<const float2*>(a.es + (int64_t)t2 * a.d + c));
+              y.x += o.x;
+              y.y += o.y;
+            }
+            reinterpret_cast<__nv_bfloat162*>(static_cast<bf16*>(a.y) + (int64_t)t2 * a.d + c)[0] = __floats2bfloat162_rn(y.x, y.y);
+          }
+        }
+      }
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+  }
+}
+
+// ---- host side ---------------------------------------------------------------------
+// 2-D tensor [rows, cols] (cols contiguous), box [box_rows, 128 bytes], 128-byte swizzle.
+bool make_map(CUtensorMap* m, bool fp8, const void* base, int64_t rows, int64_t cols, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int64_t b = fp8 ? 1 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(cols * b)};
+  const cuuint32_t box[2] = {(cuuint32_t)(kKB / b), (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP8>
+cudaError_t launch_t(const DecodeArgs& a, const DecodeMaps& maps, const TcShape& sh, int grid, size_t smem, cudaStream_t s) {
+  static std::atomic<uint64_t> attr;
+  const cudaError_t e = set_smem_limit(attr, (const void*)decode_tc_kernel<FP8>, kSmemLimit);
+  if (e != cudaSuccess) return e;
+  decode_tc_kernel<FP8><<<grid, kThreads, smem, s>>>(maps, a, sh);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool decode_tc_supported(const DecodeArgs& a) {
+  const int64_t widest = a.I > a.d ? a.I : a.d;
+  return encode_fn() != nullptr && a.E * widest < ((int64_t)1 << 31) - 256;  // TMA row coordinates
+}
+
+cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s) {
+  const bool fp8 = a.dtype == MOE_FP8;
+  TcShape sh{};
+  sh.n_cols = (int32_t)align_up(a.n, 16);
+  sh.stage_bytes = 2 * kABytes + sh.n_cols * kKB + (fp8 ? (int32_t)align_up(3 * kSfBytes, 1024) : 0);
+  const int64_t slots = align_up((int64_t)a.n * a.k * 6, 16);
+  const int64_t fit = ((int64_t)kSmemLimit - 1024 - slots - (int64_t)sizeof(Ctl)) / sh.stage_bytes;
+  sh.stages = (int32_t)(fit < kMaxStages ? fit : kMaxStages);
+  sh.slot_off = sh.stages * sh.stage_bytes;
+  sh.ctl_off = sh.slot_off + (int32_t)slots;
+  const size_t smem = 1024 + (size_t)sh.ctl_off + sizeof(Ctl);
+  if (sh.stages < 2) return cudaErrorInvalidValue;
+  DecodeMaps m;
+  const int64_t E = a.E, nk = (int64_t)a.n * a.k;
+  bool ok = make_map(&m.gate, fp8, a.w_gate, E * a.I, a.d, kRows) && make_map(&m.up, fp8, a.w_up, E * a.I, a.d, kRows) &&
+            make_map(&m.down, fp8, a.w_down, E * a.d, a.I, kRows) &&
+            make_map(&m.x, fp8, fp8 ? a.xq : a.x, a.n, a.d, sh.n_cols) && make_map(&m.h, fp8, a.h, nk, a.I, 16);
+  m.sgate = m.sup = m.gate;
+  m.sdown = m.down;
+  m.hs = m.h;
+  if (a.Is > 0)
+    ok = ok && make_map(&m.sgate, fp8, a.ws_gate, a.Is, a.d, kRows) && make_map(&m.sup, fp8, a.ws_up, a.Is, a.d, kRows) &&
+         make_map(&m.sdown, fp8, a.ws_down, a.d, a.Is, kRows) && make_map(&m.hs, fp8, a.hs, a.n, a.Is, sh.n_cols);
+  if (!ok) return cudaErrorInvalidValue;
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (sms <= 0) sms = 148;
+  return fp8 ? launch_t<true>(a, m, sh, sms, smem, s) : launch_t<false>(a, m, sh, sms, smem, s);
+}
+
+}  // namespace moe

@@ -203,6 +203,8 @@ struct DecodeArgs {
 };
 int64_t decode_counters(int32_t E, int32_t d);  // counter words
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t s);
+cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s);  // bf16 and FP8 experts
+bool decode_tc_supported(const DecodeArgs& a);
 
 // Capacity rule over the ranking on many SMs (capacity.cu): a cooperative grid, one token per
 // thread, one round per fill event. Needs capacity_grid_scratch_bytes of scratch (16-byte aligned)
