@@ -17,11 +17,11 @@
 #include "fp8.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
-#include "route_decide.cuh"
 
 namespace moe {
 namespace {
 
+constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr uint64_t kDecodeTimeoutNs = 2000000000ull;  // 2 s for any single wait
 
 // Counter words (zeroed before the launch).
@@ -31,7 +31,7 @@ enum {
   kCtrQuantDone,
   kCtrLogit,       // router units
   kCtrLogitDone,
-  kCtrToken,       // routing decisions
+  kCtrToken,       // routing decisions, a block each
   kCtrTokenDone,
   kCtrTile,        // gate/up and down tiles
   kCtrExpert = 16  // [E + 1] finished gate/up tiles per expert (E: shared), then [column ranges] finished down tiles
@@ -112,121 +112,248 @@ __device__ __forceinline__ void unpack(const uint4& raw, float (&v)[4]) {
 // Experts per router unit: the units spread over the grid.
 __host__ __device__ inline int router_unit(int E, int grid) { return (E + grid - 1) / grid; }
 
-constexpr int kRouterTokens = 4;  // tokens of one dot-product item: each weight is converted once for them
+// A binary32 value times 2^-896 as a binary64, exact for every finite value (subnormals and zeros
+// included: the fields only move): three integer operations, where the conversion instruction runs
+// at 4 lanes a clock and SM and made the logits of 64 tokens take 150 us.
+__device__ __forceinline__ double widened(float v) {
+  const int u = __float_as_int(v);
+  return __hiloint2double((u >> 3) & (int)0x8FFFFFFF, u << 29);
+}
+// A router weight gets 2^512 (two steps: 2^(896 + 512) is past the range), so that its products with
+// widened activations are 2^-384 of the true ones, far from both ends of the range.
+__device__ __forceinline__ double widened_weight(float v) { return widened(v) * 0x1p1000 * 0x1p408; }
+constexpr double kWidenLogit = 0x1p384;
 
-// Binary64 logits of experts [e0, e1) for every token, by the NW warps of a block (warp `w`; `part`:
-// NW * 2 * kRouterTokens doubles). Exact products, binary64 sums. Items are (expert, four tokens),
-// cut along d when there are fewer of them than warps; a cut item's parts are added in order.
-// `sync` is a barrier of these warps.
-template <typename T, int NW, typename Sync>
-__device__ void router_logits_unit(const DecodeArgs& a, int e0, int e1, int w, double* part, Sync sync) {
+constexpr int kRouterTokens = 4;  // tokens of one dot-product item: each weight is widened once for them
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+  return v;
+}
+
+// Binary64 logits of experts e0 and (pair) e0 + 1 for every token, by the NW warps of a block (warp
+// `w`; `part`: NW * 2 * kRouterTokens doubles). Products of bf16 values are exact, sums are binary64.
+// Items are groups of TOK tokens, cut along d when there are fewer of them than warps; a cut item's
+// parts are added in order. The loads of BATCH steps are issued before their products: a step whose
+// loads wait on branches took a memory latency per token. A row with a NaN or an infinity gets NaN
+// logits (the widening alone would take them for finite values). `sync` is a barrier of these warps.
+template <typename T, int NW, int TOK, int BATCH, typename Sync>
+__device__ void router_logits_pair(const DecodeArgs& a, int e0, bool pair, int w, double* part, Sync sync) {
   constexpr int C = Chunk<T>::N;
   const int lane = threadIdx.x & 31;
-  const int groups = (a.n + kRouterTokens - 1) / kRouterTokens;
-  const int items = (e1 - e0) * groups;
+  const int items = (a.n + TOK - 1) / TOK;
   const int cuts = items >= NW ? 1 : NW / items;
   const int chunks = a.d / C;  // d % 8 == 0
   const int per = (chunks + cuts - 1) / cuts;
+  const uint4* w0 = reinterpret_cast<const uint4*>(static_cast<const T*>(a.w_router) + (int64_t)e0 * a.d);
+  const uint4* w1 = pair ? w0 + chunks : w0;
   for (int it = w; it < items * cuts; it += NW) {
-    const int item = it / cuts, cut = it % cuts;
-    const int e = e0 + item / groups, t0 = (item % groups) * kRouterTokens;
-    const uint4* wr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.w_router) + (int64_t)e * a.d);
-    const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x));
-    double acc[kRouterTokens] = {};
+    const int item = it / cuts, cut = it % cuts, t0 = item * TOK;
+    const int last = min(TOK, a.n - t0) - 1;
+    const uint4* xr = reinterpret_cast<const uint4*>(a.x) + (int64_t)t0 * chunks;
+    double acc[2][TOK] = {};
+    float odd[2] = {}, odd_x[TOK] = {};  // NaN once a value is not finite
     const int c1 = min(chunks, (cut + 1) * per);
-#pragma unroll 2
-    for (int c = cut * per + lane; c < c1; c += 32) {
-      float wv[C];
-      unpack(__ldg(wr + c), wv);
-      double wd[C];
+    for (int c0 = cut * per; c0 < c1; c0 += 32 * BATCH) {
+      uint4 r0[BATCH], r1[BATCH], rx[BATCH][TOK];
 #pragma unroll
-      for (int j = 0; j < C; ++j) wd[j] = (double)wv[j];
+      for (int b = 0; b < BATCH; ++b) {
+        const int c = c0 + 32 * b + lane;
+        const bool in = c < c1;
+        r0[b] = in ? __ldg(w0 + c) : make_uint4(0, 0, 0, 0);
+        r1[b] = in ? __ldg(w1 + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int q = 0; q < kRouterTokens; ++q) {
-        if (t0 + q >= a.n) break;
-        float xv[C];
-        unpack(__ldg(xr + (int64_t)(t0 + q) * chunks + c), xv);
+        for (int q = 0; q < TOK; ++q)  // past the last token: its row again, not stored
+          rx[b][q] = in ? __ldg(xr + (int64_t)min(q, last) * chunks + c) : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-        for (int j = 0; j < C; ++j) acc[q] = fma((double)xv[j], wd[j], acc[q]);
+      for (int b = 0; b < BATCH; ++b) {
+        float v0[C], v1[C];
+        unpack(r0[b], v0);
+        unpack(r1[b], v1);
+        double d0[C], d1[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          d0[j] = widened_weight(v0[j]);
+          d1[j] = widened_weight(v1[j]);
+          odd[0] = fmaf(v0[j], 0.0f, odd[0]);
+          odd[1] = fmaf(v1[j], 0.0f, odd[1]);
+        }
+#pragma unroll
+        for (int q = 0; q < TOK; ++q) {
+          float xv[C];
+          unpack(rx[b][q], xv);
+#pragma unroll
+          for (int j = 0; j < C; ++j) {
+            const double xd = widened(xv[j]);
+            acc[0][q] = fma(xd, d0[j], acc[0][q]);
+            acc[1][q] = fma(xd, d1[j], acc[1][q]);
+            odd_x[q] = fmaf(xv[j], 0.0f, odd_x[q]);
+          }
+        }
       }
     }
 #pragma unroll
-    for (int q = 0; q < kRouterTokens; ++q) {
-      if (t0 + q >= a.n) break;
-      const double s = warp_sum(acc[q]);
-      if (lane == 0) {
+    for (int q = 0; q < TOK; ++q)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const double s = warp_sum(acc[p][q] * kWidenLogit + (double)(odd[p] + odd_x[q]));
+        if (lane != 0 || (p && !pair) || q > last) continue;
         if (cuts == 1)
-          a.logits[(int64_t)(t0 + q) * a.E + e] = s;
+          a.logits[(int64_t)(t0 + q) * a.E + e0 + p] = s;
         else
-          part[it * kRouterTokens + q] = s;  // it < items * cuts <= NW
+          part[(it * 2 + p) * TOK + q] = s;  // it < items * cuts <= NW
       }
-    }
   }
   if (cuts == 1) return;
   sync();
   if (w == 0)
-    for (int i = lane; i < items * kRouterTokens; i += 32) {
-      const int item = i / kRouterTokens, q = i % kRouterTokens;
-      const int t = (item % groups) * kRouterTokens + q;
-      if (t >= a.n) continue;
+    for (int i = lane; i < items * 2 * TOK; i += 32) {
+      const int item = i / (2 * TOK), p = i / TOK % 2, q = i % TOK;
+      const int t = item * TOK + q;
+      if (t >= a.n || (p && !pair)) continue;
       double s = 0.0;
-      for (int cut = 0; cut < cuts; ++cut) s += part[(item * cuts + cut) * kRouterTokens + q];
-      a.logits[(int64_t)t * a.E + e0 + item / groups] = s;
+      for (int cut = 0; cut < cuts; ++cut) s += part[((item * cuts + cut) * 2 + p) * TOK + q];
+      a.logits[(int64_t)t * a.E + e0 + p] = s;
     }
-  sync();  // `part` is the next unit's
+  sync();  // `part` is the next pair's
 }
 
-// Scratch of one deciding warp.
-struct DecideScratch {
-  int16_t rank[kMaxExperts];
-  int idx[kMaxTopK];
+template <typename T, int NW, typename Sync>
+__device__ void router_logits_unit(const DecodeArgs& a, int e0, int e1, int w, double* part, Sync sync) {
+  for (int e = e0; e < e1; e += 2) {
+    if (a.n == 1)
+      router_logits_pair<T, NW, 1, 4>(a, e, e + 1 < e1, w, part, sync);
+    else
+      router_logits_pair<T, NW, kRouterTokens, 2>(a, e, e + 1 < e1, w, part, sync);
+  }
+}
+
+// Order-preserving key of a double: a larger value has a larger key; never 0. -0 is taken as +0
+// first, so that the two have one key as they compare equal.
+__device__ __forceinline__ unsigned long long order_key(double v) {
+  const unsigned long long b = (unsigned long long)__double_as_longlong(v + 0.0);
+  const unsigned long long key = (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+  return key ? key : 1ull;
+}
+
+struct __align__(16) DecideScratch {
+  unsigned long long key[kMaxExperts];  // selection values; 0: not eligible
+  unsigned long long top[kMaxExperts];  // each warp's k best keys and experts, best first
+  int16_t top_e[kMaxExperts];
+  unsigned long long group[kMaxGroups];
+  double best[2][kMaxGroups];
+  double part[8];
   double val[kMaxTopK];
-  unsigned long long keys[kMaxExperts];
+  int idx[kMaxTopK];
 };
 
-// Token t's experts and gates from its binary64 logits, by one warp.
-template <int EPL>
-__device__ void decide_token(const DecodeArgs& a, int t, DecideScratch* sc) {
-  const int lane = threadIdx.x & 31;
-  RouteArgs r{};
-  r.bias = a.bias;
-  r.E = a.E;
-  r.k = a.k;
-  r.G = a.G;
-  r.topk_group = a.topk_group;
-  r.score_fn = a.score_fn;
-  r.renorm = a.renorm;
-  r.rsf = a.rsf;
-  double l[EPL];
-  uint32_t exact = 0;
+// The block's largest value (SUM: sum) of v over 256 threads, in a fixed order.
+template <bool SUM, typename Sync>
+__device__ __noinline__ double block_reduce(double v, double* part, int tid, Sync sync) {
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = lane + 32 * j;
-    l[j] = e < a.E ? __ldcg(a.logits + (int64_t)t * a.E + e) : 0.0;
-    exact |= 1u << j;
+  for (int off = 16; off; off >>= 1) {
+    const double o = __shfl_xor_sync(kFull, v, off);
+    v = SUM ? v + o : fmax(v, o);
   }
-  int nr = 0;
-  uint32_t refine = 0;
-  decide<EPL>(r, l, exact, 0.0, sc->rank, &nr, &refine, sc->keys);  // exact logits: every comparison is certain
-  if (lane < a.k) sc->idx[lane] = lane < nr ? (int)sc->rank[lane] : -1;
-  __syncwarp();
-  const float g = gates<EPL>(r, l, sc->idx, sc->val);
-  if (lane < a.k) {
-    a.topk_idx[t * a.k + lane] = sc->idx[lane];
-    a.topk_w[t * a.k + lane] = g;
-  }
-  __syncwarp();
+  if ((tid & 31) == 0) part[tid >> 5] = v;
+  sync();
+  v = part[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) v = SUM ? v + part[i] : fmax(v, part[i]);
+  sync();
+  return v;
 }
 
-__device__ inline void decide_token_any(const DecodeArgs& a, int t, DecideScratch* sc) {
-  if (a.E <= 32)
-    decide_token<1>(a, t, sc);
-  else if (a.E <= 64)
-    decide_token<2>(a, t, sc);
-  else if (a.E <= 128)
-    decide_token<4>(a, t, sc);
-  else
-    decide_token<8>(a, t, sc);
+// Token t's experts and gates from its binary64 logits (definitions in router.cu), by 256 threads,
+// an expert each: an expert's place is the number of better keys, counted over shared memory, first
+// in its warp, then for each warp's k best among those of all. `bias` is the thread's expert's. One
+// warp walking top-k rounds with eight experts a lane took 49 us at E = 256: its code does not fit
+// the instruction cache, and a block runs it once.
+template <typename Sync>
+__device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScratch* sc, int tid, Sync sync) {
+  const int e = tid;
+  const bool live = e < a.E;
+  const double l = live ? __ldcg(a.logits + (int64_t)t * a.E + e) : 0.0;
+  double score = l;  // what the gate is made of
+  if (a.score_fn == MOE_SCORE_SIGMOID)
+    score = 1.0 / (1.0 + exp(-l));
+  else if (a.score_fn == MOE_SCORE_SQRTSOFTPLUS)
+    score = sqrt(fmax(l, 0.0) + log1p(exp(-fabs(l))));
+  const double sel = score + (double)bias;
+  unsigned long long key = live ? order_key(sel) : 0ull;
+  sc->key[e] = key;
+  sync();
+  if (a.G > 1) {
+    // the two best of each group, then the groups by their sum (ties: the lower group)
+    const int per = a.E / a.G, g = e / per;
+    if (live) {
+      int better = 0;
+      for (int f = g * per; f < (g + 1) * per; ++f) {
+        const unsigned long long o = sc->key[f];
+        better += o > key || (o == key && f < e);
+      }
+      if (better < 2) sc->best[better][g] = sel;
+      if (per == 1) sc->best[1][g] = -INFINITY;
+    }
+    sync();
+    if (tid < a.G) sc->group[tid] = order_key(sc->best[0][tid] + sc->best[1][tid]);
+    sync();
+    if (live) {
+      const unsigned long long mine = sc->group[g];
+      int better = 0;
+      for (int h = 0; h < a.G; ++h) better += sc->group[h] > mine || (sc->group[h] == mine && h < g);
+      if (better >= a.topk_group) sc->key[e] = key = 0ull;
+    }
+    sync();
+  }
+  if (a.score_fn == MOE_SCORE_SOFTMAX) {
+    const double m = block_reduce<false>(live ? l : -INFINITY, sc->part, tid, sync);
+    score = live ? exp(l - m) : 0.0;
+    score /= block_reduce<true>(score, sc->part, tid, sync);
+  }
+  {
+    const int w0 = tid & ~31, per_warp = min(a.k, 32);
+    int better = 0;
+    if (w0 < a.E) {
+#pragma unroll 8
+      for (int f = 0; f < 32; ++f) {
+        const unsigned long long o = sc->key[w0 + f];
+        better += o > key || (o == key && w0 + f < e);
+      }
+    } else {
+      better = tid & 31;
+    }
+    if (better < per_warp) {  // experts past E and groups left out come last, with key 0
+      sc->top[(w0 >> 5) * per_warp + better] = key;
+      sc->top_e[(w0 >> 5) * per_warp + better] = (int16_t)e;
+    }
+    sync();
+    if (key && better < per_warp) {
+      const int count = (a.E + 31) / 32 * per_warp;
+      better = 0;
+#pragma unroll 8
+      for (int f = 0; f < count; ++f) {
+        const unsigned long long o = sc->top[f];
+        better += o > key || (o == key && sc->top_e[f] < e);
+      }
+      if (better < a.k) {
+        sc->idx[better] = e;
+        sc->val[better] = score;
+      }
+    }
+  }
+  sync();
+  if (tid < 32) {
+    const double v = tid < a.k ? sc->val[tid] : 0.0;
+    const double denom = a.renorm ? warp_sum(v) : 1.0;
+    if (tid < a.k) {
+      a.topk_idx[t * a.k + tid] = sc->idx[tid];
+      a.topk_w[t * a.k + tid] = (float)(v / denom * (double)a.rsf);
+    }
+  }
+  sync();
 }
 
 // ---- plan --------------------------------------------------------------------------
@@ -247,13 +374,16 @@ __device__ __forceinline__ int slot_row(const DecodePlan& p, int e, int t) {
   return p.off[e] + __popcll(p.mask[e] & ((1ull << t) - 1ull));
 }
 
-// Built by NT threads (tid 0 .. NT-1, warp 0 among them) from the finished decisions.
+// Built by NT threads (tid 0 .. NT-1, warp 0 among them) from the finished decisions; slot_w and
+// slot_r (given: [n * k]) receive each slot's gate and its row (0xFFFF: none). The masks are zero.
 template <int NT, typename Sync>
-__device__ void build_plan(const DecodeArgs& a, DecodePlan* p, int tid, Sync sync) {
-  for (int e = tid; e < kMaxExperts; e += NT) p->mask[e] = 0ull;
-  sync();
-  for (int s = tid; s < a.n * a.k; s += NT) {
-    const int e = __ldcg(a.topk_idx + s);
+__device__ void build_plan(const DecodeArgs& a, DecodePlan* p, float* slot_w, uint16_t* slot_r, int tid, Sync sync) {
+  const int slots = a.n * a.k;
+  // the first NT slots stay in registers: most batches have no more
+  const int e0 = tid < slots ? __ldcg(a.topk_idx + tid) : -1;
+  const float g0 = tid < slots ? __ldcg(a.topk_w + tid) : 0.0f;
+  for (int s = tid; s < slots; s += NT) {
+    const int e = s == tid ? e0 : __ldcg(a.topk_idx + s);
     if (e >= 0) atomicOr(&p->mask[e], 1ull << (s / a.k));
   }
   sync();
@@ -266,18 +396,17 @@ __device__ void build_plan(const DecodeArgs& a, DecodePlan* p, int tid, Sync syn
       rows += c[j];
       live += c[j] > 0;
     }
-    int r = rows, v = live;
+    int both = rows << 16 | live;  // at most 2048 rows, 256 experts
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int ro = __shfl_up_sync(kFull, r, off), vo = __shfl_up_sync(kFull, v, off);
-      if (tid >= off) r += ro, v += vo;
+      const int o = __shfl_up_sync(kFull, both, off);
+      if (tid >= off) both += o;
     }
     if (tid == 31) {
-      p->off[kMaxExperts] = r;
-      p->n_act = v;
+      p->off[kMaxExperts] = both >> 16;
+      p->n_act = both & 0xFFFF;
     }
-    r -= rows;
-    v -= live;
+    int r = (both >> 16) - rows, v = (both & 0xFFFF) - live;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       p->off[tid * PER + j] = r;
@@ -286,6 +415,12 @@ __device__ void build_plan(const DecodeArgs& a, DecodePlan* p, int tid, Sync syn
     }
   }
   sync();
+  if (slot_w)
+    for (int s = tid; s < slots; s += NT) {
+      const int e = s == tid ? e0 : __ldcg(a.topk_idx + s);
+      slot_w[s] = s == tid ? g0 : __ldcg(a.topk_w + s);
+      slot_r[s] = e < 0 ? (uint16_t)0xFFFF : (uint16_t)slot_row(*p, e, s / a.k);
+    }
 }
 
 // counts and diag of the call, by one block.

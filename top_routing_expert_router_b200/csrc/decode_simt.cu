@@ -41,8 +41,8 @@ struct Types<MOE_FP8> {
 struct Shared {
   DecodePlan plan;
   union {
-    DecideScratch decide[kWarps];
-    double part[kWarps * kRouterTokens];
+    DecideScratch decide;
+    double part[kWarps * 2 * kRouterTokens];
     float h[MOE_DECODE_MAX_TOKENS][128];
   };
   uint8_t tok[MOE_DECODE_MAX_TOKENS];
@@ -137,15 +137,16 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
     router_logits_unit<Out, kWarps>(a, u * unit, min(a.E, (u + 1) * unit), warp, sm.part, sync);
     finish(a.ctr + kCtrLogitDone);
   }
-  for (int u; (u = claim(kCtrToken)) * kWarps < a.n;) {
+  for (int e = tid; e < kMaxExperts; e += kThreads) sm.plan.mask[e] = 0ull;
+  const float bias = a.bias && tid < a.E ? __ldg(a.bias + tid) : 0.0f;
+  for (int t; (t = claim(kCtrToken)) < a.n;) {
     if (!wait(a.ctr + kCtrLogitDone, units)) return;
-    const int t = u * kWarps + warp;
-    if (t < a.n) decide_token_any(a, t, &sm.decide[warp]);
+    decide_token(a, t, bias, &sm.decide, tid, sync);
     finish(a.ctr + kCtrTokenDone);
   }
-  if (!wait(a.ctr + kCtrTokenDone, (a.n + kWarps - 1) / kWarps)) return;
+  if (!wait(a.ctr + kCtrTokenDone, a.n)) return;
   if (quant && !wait(a.ctr + kCtrQuantDone, quants)) return;
-  build_plan<kThreads>(a, &sm.plan, tid, sync);
+  build_plan<kThreads>(a, &sm.plan, nullptr, nullptr, tid, sync);
   if (blockIdx.x == 0) write_counts<kThreads>(a, sm.plan, tid);
 
   const int shared = a.Is > 0;

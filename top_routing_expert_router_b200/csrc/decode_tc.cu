@@ -34,6 +34,7 @@ using namespace ptx;
 
 constexpr int kThreads = 384;
 constexpr int kRouterWarps = 8, kRouterThreads = 32 * kRouterWarps;  // warps 4..11
+static_assert(kRouterThreads == kMaxExperts, "a router thread per expert");
 constexpr int kRows = 128;                  // weight rows of an MMA
 constexpr int kKB = 128;                    // bytes of k per stage and row
 constexpr int kABytes = kRows * kKB;        // one weight block
@@ -62,7 +63,7 @@ struct __align__(16) Ctl {
   int32_t routed;              // every token's decision was seen
   int32_t last;
   float4 amax[16];             // FP8: a column's largest |h| per epilogue warp
-  double part[kRouterWarps * kRouterTokens];
+  double part[kRouterWarps * 2 * kRouterTokens];
   DecideScratch decide;
   DecodePlan plan;
 };
@@ -429,6 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     auto sync = [] { named_sync<1, kRouterThreads>(); };
     const int quants = FP8 && a.quantize ? (a.n * (a.d / 128) + kRouterWarps - 1) / kRouterWarps : 0;
     const int unit = router_unit(a.E, gridDim.x), units = (a.E + unit - 1) / unit;
+    ctl->plan.mask[tid] = 0ull;
+    const float bias = a.bias && tid < a.E ? __ldg(a.bias + tid) : 0.0f;
     for (;;) {  // E4M3 tiles of x, then logits
       if (tid == 0) ctl->ticket = atomicAdd(a.ctr + kCtrLogit, 1);
       sync();
@@ -446,35 +449,32 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
       sync();
       if (tid == 0) add_release(a.ctr + (u < quants ? kCtrQuantDone : kCtrLogitDone), 1);
     }
+    sync();  // everyone has read the last ticket
     bool ok = true;
-    if (rw == 0) {  // one warp a block decides tokens: there are more blocks than tokens
-      for (;;) {
-        int t = 0;
-        if (lane == 0) t = atomicAdd(a.ctr + kCtrToken, 1);
-        t = __shfl_sync(kFull, t, 0);
-        if (t >= a.n) break;
-        if (lane == 0) ok = wait_counter(a.ctr + kCtrLogitDone, units, a.ctr, a.status);
-        if (!(ok = __shfl_sync(kFull, (int)ok, 0) != 0)) break;
-        decide_token_any(a, t, &ctl->decide);
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) add_release(a.ctr + kCtrTokenDone, 1);
+    auto all_ok = [&](bool v) {  // thread 0's answer for all: the barriers count every router warp
+      if (tid == 0) ctl->routed = v;
+      sync();
+      return ctl->routed != 0;
+    };
+    for (;;) {
+      if (tid == 0) {
+        ctl->ticket = atomicAdd(a.ctr + kCtrToken, 1);
+        if (ctl->ticket < a.n) ok = wait_counter(a.ctr + kCtrLogitDone, units, a.ctr, a.status);
       }
-      if (lane == 0) {
-        if (ok) ok = wait_counter(a.ctr + kCtrTokenDone, a.n, a.ctr, a.status);
-        if (!ok) atomicExch(&ctl->abort, 1);
-        ctl->routed = ok;
-      }
+      ok = all_ok(ok);
+      const int t = ctl->ticket;
+      if (!ok || t >= a.n) break;
+      decide_token(a, t, bias, &ctl->decide, tid, sync);
+      __threadfence();
+      sync();
+      if (tid == 0) add_release(a.ctr + kCtrTokenDone, 1);
     }
-    sync();
-    ok = ctl->routed != 0;  // one answer for all: the barriers below count every router warp
+    if (tid == 0 && ok) ok = wait_counter(a.ctr + kCtrTokenDone, a.n, a.ctr, a.status);
+    if (tid == 0 && !ok) atomicExch(&ctl->abort, 1);
+    sync();  // everyone has read the last answer
+    ok = all_ok(ok);
     if (ok) {
-      build_plan<kRouterThreads>(a, &ctl->plan, tid, sync);
-      for (int s = tid; s < a.n * a.k; s += kRouterThreads) {
-        const int e = __ldcg(a.topk_idx + s);
-        slot_w[s] = __ldcg(a.topk_w + s);
-        slot_r[s] = e < 0 ? (uint16_t)0xFFFF : (uint16_t)slot_row(ctl->plan, e, s / a.k);
-      }
+      build_plan<kRouterThreads>(a, &ctl->plan, slot_w, slot_r, tid, sync);
       sync();
       if (lane == 0) mbar_arrive(&ctl->plan_ready);
       if (blockIdx.x == 0 && rw >= 4) write_counts<kRouterThreads - 128>(a, ctl->plan, tid - 128);
