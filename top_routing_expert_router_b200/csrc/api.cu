@@ -22,7 +22,7 @@ struct Plan {
   size_t diag, logits, rq, rc, ranking, capg, blk, idx, w, counts, offsets, perm, dest, xperm, h, eo, shh, sh, shoff, sched;
   size_t xq, sfx, hq, sfh, xsq, sfxs, hsq, sfhs;  // FP8 experts: E4M3 activations and their scale blocks
   size_t sfb, sfbs;  // FP8 SM-pair GEMMs: B scale blocks (routed, shared experts)
-  size_t dctr, dlog, deo, des, dhs, dhss, dxs;  // moe_layer_decode: counters, binary64 logits, binary32 expert outputs, scale bytes
+  size_t dctr, dlog, dgu, deo, des, dhs, dhss, dxs;  // moe_layer_decode: counters, binary64 logits, binary32 parts and outputs, scale bytes
   size_t ep_off;  // expert parallelism: receive offsets of the rank's own experts
   size_t total;
   bool batched;   // the two-kernel router queues its undecided tokens for launch_refine (rq, rc reserved)
@@ -102,7 +102,9 @@ Plan make_plan(const moe_config& c, int64_t n, int32_t ep_world = 0, int64_t ep_
   p.diag = take(sizeof(moe_diag));
   // the counters right behind the status word: one memset clears both
   const bool few = !ep && n > 0 && n <= MOE_DECODE_MAX_TOKENS && c.cap_policy == MOE_CAP_NONE;
-  p.dctr = take(few ? (size_t)decode_counters(c.n_routed, c.d_model) * 4 : 0);
+  const DecodeSplits cut = few ? decode_splits(n, c.d_model, c.n_routed, c.top_k, c.moe_intermediate_size, (int32_t)Is, c.dtype)
+                               : DecodeSplits{};
+  p.dctr = take(few ? (size_t)decode_counters(cut, c.d_model, c.n_routed, c.moe_intermediate_size, (int32_t)Is) * 4 : 0);
   p.logits = take((size_t)router_splits(c, n) * n * logits_ld(c) * 4);
   // the queue of tokens left to the binary64 router (one-pass router, or the first pass of the
   // two-kernel router), and their candidate experts: four counters, the candidate table, its
@@ -148,8 +150,9 @@ Plan make_plan(const moe_config& c, int64_t n, int32_t ep_world = 0, int64_t ep_
   p.sfbs = take(fp8 && Is > 0 ? sfb_bytes(1, Is, d) : 0);
   p.ep_off = take(ep ? (size_t)(fg + 1) * 4 : 0);
   p.dlog = take(few ? (size_t)n * c.n_routed * 8 : 0);
-  p.deo = take(few ? (size_t)nk * d * 4 : 0);
-  p.des = take(few && Is > 0 ? (size_t)n * d * 4 : 0);
+  p.dgu = take(few && (cut.s1 > 1 || cut.s1s > 1) ? (size_t)2 * (cut.s1 * nk * I + cut.s1s * n * Is) * 4 : 0);
+  p.deo = take(few ? (size_t)cut.s2 * nk * d * 4 : 0);
+  p.des = take(few && Is > 0 ? (size_t)cut.s2s * n * d * 4 : 0);
   p.dxs = take(few && fp8 ? (size_t)n * (d / 128) : 0);
   p.dhs = take(few && fp8 ? (size_t)nk * (I / 128) : 0);
   p.dhss = take(few && fp8 && Is > 0 ? (size_t)n * (Is / 128) : 0);
@@ -1004,6 +1007,7 @@ moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, con
   a.quantize = fp8 && !given;
   a.xq = given ? const_cast<uint8_t*>(x_codes_opt) : c.at<uint8_t>(c.p.xq);
   a.xs = given ? const_cast<uint8_t*>(x_scale_bytes_opt) : c.at<uint8_t>(c.p.dxs);
+  a.cut = decode_splits(n, a.d, a.E, a.k, a.I, a.Is, a.dtype);
   a.logits = c.at<double>(c.p.dlog);
   a.topk_idx = topk_idx_opt ? topk_idx_opt : c.at<int32_t>(c.p.idx);
   a.topk_w = topk_w_opt ? topk_w_opt : c.at<float>(c.p.w);
@@ -1011,6 +1015,7 @@ moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, con
   a.hs = fp8 ? c.at<void>(c.p.hsq) : c.at<void>(c.p.shh);
   a.h_scale = c.at<uint8_t>(c.p.dhs);
   a.hs_scale = c.at<uint8_t>(c.p.dhss);
+  a.gu = c.at<float>(c.p.dgu);
   a.eo = c.at<float>(c.p.deo);
   a.es = c.at<float>(c.p.des);
   a.y = y;
@@ -1020,7 +1025,8 @@ moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, con
   a.status = c.status();
   const bool tensor = f.dtype != MOE_F32;
   if (tensor && !decode_tc_supported(a)) return MOE_ERR_UNSUPPORTED;
-  MOE_CUDA(cudaMemsetAsync(c.ws, 0, c.p.dctr + (size_t)decode_counters(a.E, a.d) * 4, c.s));
+  a.clear = c.ws;
+  a.clear_bytes = (int32_t)align_up((int64_t)c.p.dctr + decode_counters(a.cut, a.d, a.E, a.I, a.Is) * 4, 16);
   return cuda_status(tensor ? launch_decode_tc(a, c.s) : launch_decode_simt(a, c.s));
 }
 

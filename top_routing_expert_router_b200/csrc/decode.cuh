@@ -34,8 +34,10 @@ enum {
   kCtrToken,       // routing decisions, a block each
   kCtrTokenDone,
   kCtrTile,        // gate/up and down tiles
-  kCtrExpert = 16  // [E + 1] finished gate/up tiles per expert (E: shared), then [column ranges] finished down tiles
+  kCtrExpert = 16  // [E + 1] finished gate/up tiles per expert (E: shared), then [column ranges] finished down
+                   // tiles, then (gate/up tiles cut along k) [E * tiles + shared tiles] finished parts
 };
+constexpr int kMinColumns = 32;  // output columns of a down tile, at least
 
 __device__ __forceinline__ int ld_acquire(const int32_t* p) {
   int v;
@@ -375,7 +377,7 @@ __device__ __forceinline__ int slot_row(const DecodePlan& p, int e, int t) {
 }
 
 // Built by NT threads (tid 0 .. NT-1, warp 0 among them) from the finished decisions; slot_w and
-// slot_r (given: [n * k]) receive each slot's gate and its row (0xFFFF: none). The masks are zero.
+// slot_r (given: [n * k]) receive each slot's gate and its row. The masks are zero.
 template <int NT, typename Sync>
 __device__ void build_plan(const DecodeArgs& a, DecodePlan* p, float* slot_w, uint16_t* slot_r, int tid, Sync sync) {
   const int slots = a.n * a.k;
@@ -384,7 +386,7 @@ __device__ void build_plan(const DecodeArgs& a, DecodePlan* p, float* slot_w, ui
   const float g0 = tid < slots ? __ldcg(a.topk_w + tid) : 0.0f;
   for (int s = tid; s < slots; s += NT) {
     const int e = s == tid ? e0 : __ldcg(a.topk_idx + s);
-    if (e >= 0) atomicOr(&p->mask[e], 1ull << (s / a.k));
+    atomicOr(&p->mask[e], 1ull << (s / a.k));
   }
   sync();
   if (tid < 32) {
@@ -419,7 +421,7 @@ __device__ void build_plan(const DecodeArgs& a, DecodePlan* p, float* slot_w, ui
     for (int s = tid; s < slots; s += NT) {
       const int e = s == tid ? e0 : __ldcg(a.topk_idx + s);
       slot_w[s] = s == tid ? g0 : __ldcg(a.topk_w + s);
-      slot_r[s] = e < 0 ? (uint16_t)0xFFFF : (uint16_t)slot_row(*p, e, s / a.k);
+      slot_r[s] = (uint16_t)slot_row(*p, e, s / a.k);
     }
 }
 
@@ -434,7 +436,7 @@ __device__ void write_counts(const DecodeArgs& a, const DecodePlan& p, int tid) 
     most = __reduce_max_sync(kFull, most);
     if (tid == 0) {
       a.diag->overflowed = 0;
-      a.diag->dropped = a.n * a.k - p.off[kMaxExperts];
+      a.diag->dropped = 0;
       a.diag->refined_tokens = 0;
       a.diag->max_load = most;
       a.diag->refined_logits = 0;

@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kTokens = 8;     // token rows a weight row is multiplied with in one pass
-constexpr int kColumns = 32;   // output columns of a down tile
+constexpr int kColumns = kMinColumns;  // output columns of a down tile
 
 template <int DT>
 struct Types;
@@ -244,7 +244,6 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
       float s = 0.0f;
       for (int j = 0; j < a.k; ++j) {
         const int ej = __ldcg(a.topk_idx + t2 * a.k + j);
-        if (ej < 0) continue;
         s = fmaf(__ldcg(a.topk_w + t2 * a.k + j), __ldcg(a.eo + (int64_t)slot_row(sm.plan, ej, t2) * a.d + c), s);
       }
       if (shared) s += __ldcg(a.es + (int64_t)t2 * a.d + c);
@@ -258,13 +257,13 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> attr;
   cudaError_t e = set_smem_limit(attr, (const void*)decode_simt_kernel<DT>, sizeof(Shared));
   if (e != cudaSuccess) return e;
+  e = cudaMemsetAsync(a.clear, 0, (size_t)a.clear_bytes, s);
+  if (e != cudaSuccess) return e;
   decode_simt_kernel<DT><<<148 * 2, kThreads, sizeof(Shared), s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
-
-int64_t decode_counters(int32_t E, int32_t d) { return kCtrExpert + E + 1 + ceil_div(d, kColumns); }
 
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t s) {
   if (a.dtype == MOE_F32) return launch_t<MOE_F32>(a, s);

@@ -46,6 +46,13 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSfCol0 = 256;           // after two pairs of accumulators of at most 64 columns
 constexpr uint32_t kSfCols = 12;            // per slot: D0's rows, D1's rows, the tokens
 constexpr size_t kSmemLimit = 232448;
+// Tiles are cut along k until there are about this many, in parts of at least kMinPart k blocks. Few
+// experts (a token or two) leave fewer tiles than SMs, and one SM draws at most about 65 GB/s. The
+// routed gate/up tiles: a part costs a round trip through L2 (DeepSeek-V3 shapes, one token, 128
+// tiles: FP8 99 us whole, 97 in two parts; 8 experts of 16 tiles, top-1: 81 us whole, 44 in ten). The
+// shared ones get a part for every SM, as they stream while the router runs. Down tiles join their
+// parts in the combine (Mixtral shapes, one token, 32 tiles of 7.3 MB: 201 us whole, 135 in ten parts).
+constexpr int kTiles1 = 148, kTiles2 = 296, kMinPart = 8, kMaxParts = 16;
 
 struct __align__(16) Ctl {
   uint64_t full[kMaxStages];   // weights' and tokens' arrivals
@@ -132,12 +139,45 @@ __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint
 __device__ __forceinline__ void sf_copy(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
+// A weight tile's copy: each weight is read once a call, so its lines leave L2 first and the rest
+// (instructions, x, h, router weights) stays.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4}], "
+      "[%2], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
+
 // Orders generic writes before, and async-proxy (TMA) reads after, across the release/acquire pair between them.
 __device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 template <int ID, int COUNT>
 __device__ __forceinline__ void named_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(COUNT) : "memory");
+}
+
+// Four columns of each of two accumulators (32 lanes).
+__device__ __forceinline__ void tmem_ld4x2(uint32_t a0, uint32_t a1, float (&v0)[4], float (&v1)[4]) {
+  uint32_t x[4], y[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(a0));
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+               : "r"(a1));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v0[i] = __uint_as_float(x[i]);
+    v1[i] = __uint_as_float(y[i]);
+  }
 }
 
 // Barrier of COUNT threads that tells each whether all of them came with `v`.
@@ -161,7 +201,9 @@ struct Tile {
   int r0;       // first weight row (down: output column) of the tile
   int down;
   int Ie;       // hidden width of the expert
-  int row0, m;  // its token rows: slots row0 .. row0 + m (shared: every token)
+  int part, parts;  // which part of the k axis, of how many
+  int kb0, kb1; // its k blocks
+  int row0, m;  // the expert's token rows: slots row0 .. row0 + m (shared: every token)
   unsigned long long mask;
 };
 
@@ -174,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + sh.ctl_off);
   float* slot_w = reinterpret_cast<float*>(smem + sh.slot_off);           // [n * k] gates
-  uint16_t* slot_r = reinterpret_cast<uint16_t*>(slot_w + a.n * a.k);     // [n * k] expert output rows (0xFFFF: none)
+  uint16_t* slot_r = reinterpret_cast<uint16_t*>(slot_w + a.n * a.k);     // [n * k] expert output rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int N = sh.n_cols, stages = sh.stages;
   const int shared = a.Is > 0;
@@ -210,31 +252,44 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
   __syncthreads();
   fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero, earlier kernels' writes visible
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_try(smem_u32(bar), parity) || mbar_wait(bar, parity, ctl, a.ctr, a.status);
   };
+  const int count1 = tiles1 * a.cut.s1, count1s = tiles1s * a.cut.s1s;  // an expert's gate/up tiles, parts counted
+  const int count2 = tiles2 * a.cut.s2, count2s = shared * tiles2 * a.cut.s2s;
   auto tile_of = [&](int t) {
     Tile tl;
-    const int first2 = t < tiles1s ? INT_MAX : tiles1s + ctl->plan.n_act * tiles1;  // the plan is ready past the first tiles
+    const int first2 = t < count1s ? INT_MAX : count1s + ctl->plan.n_act * count1;  // the plan is ready past the first tiles
     tl.down = t >= first2;
-    int u;
+    int u, local, parts, per;
     if (tl.down) {
-      u = (t - first2) / tiles2 - shared;
-      tl.r0 = (t - first2) % tiles2 * kColumns;
+      local = t - first2;
+      u = local < count2s ? -1 : (local - count2s) / count2;
+      local = u < 0 ? local : (local - count2s) % count2;
+      parts = u < 0 ? a.cut.s2s : a.cut.s2;
+      per = u < 0 ? a.cut.per2s : a.cut.per2;
+      tl.r0 = local / parts * kColumns;
     } else {
-      u = t < tiles1s ? -1 : (t - tiles1s) / tiles1;
-      tl.r0 = (u < 0 ? t : (t - tiles1s) % tiles1) * kRows;
+      u = t < count1s ? -1 : (t - count1s) / count1;
+      local = u < 0 ? t : (t - count1s) % count1;
+      parts = u < 0 ? a.cut.s1s : a.cut.s1;
+      per = u < 0 ? a.cut.per1s : a.cut.per1;
+      tl.r0 = local / parts * kRows;
     }
+    tl.part = local % parts;
+    tl.parts = parts;
     tl.e = u < 0 ? a.E : ctl->plan.act[u];
     tl.Ie = u < 0 ? a.Is : a.I;
+    tl.kb0 = tl.part * per;
+    tl.kb1 = min(tl.kb0 + per, ((tl.down ? tl.Ie : a.d) + KE - 1) / KE);
     tl.mask = u < 0 ? token_mask(a.n) : ctl->plan.mask[tl.e];
     tl.row0 = u < 0 ? 0 : ctl->plan.off[tl.e];
     tl.m = __popcll(tl.mask);
     return tl;
   };
-  // Stages of a tile, and whether its second weight block has any row.
-  auto k_blocks = [&](const Tile& tl) { return ((tl.down ? tl.Ie : a.d) + KE - 1) / KE; };
+  // Whether a tile's second weight block has any row.
   auto two_blocks = [&](const Tile& tl) { return !tl.down || tl.r0 + kRows < a.d; };
   // Token columns of a tile: all of them, or a routed down tile's own rows.
   auto columns = [&](const Tile& tl) { return tl.down && tl.e < a.E ? (tl.m + 15) & ~15 : N; };
@@ -245,12 +300,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
       int stage = 0, q = 0;
       uint32_t phase = 0, qphase = 0, armed = 0;
       bool ok = true;
+      const uint64_t policy = evict_first_policy();
       int total = INT_MAX, next = atomicAdd(a.ctr + kCtrTile, 1);
       while (ok) {
         const int t = next;
-        if (t >= tiles1s && total == INT_MAX) {
+        if (t >= count1s && total == INT_MAX) {
           if (!(ok = wait(&ctl->plan_ready, 0))) break;
-          total = tiles1s + ctl->plan.n_act * tiles1 + (ctl->plan.n_act + shared) * tiles2;
+          total = count1s + count2s + ctl->plan.n_act * (count1 + count2);
         }
         if (!(ok = wait(&ctl->tile_empty[q], qphase ^ 1u))) break;
         ctl->tile[q] = t < total ? t : -1;
@@ -263,13 +319,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         const CUtensorMap* m0 = tl.down ? (s ? &maps.sdown : &maps.down) : (s ? &maps.sgate : &maps.gate);
         const CUtensorMap* m1 = tl.down ? m0 : (s ? &maps.sup : &maps.up);
         const int y0 = (s ? 0 : tl.e * (tl.down ? a.d : a.I)) + tl.r0, y1 = tl.down ? y0 + kRows : y0;
-        const int nkb = k_blocks(tl);
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
           if (!(ok = wait(&ctl->empty[stage], phase ^ 1u))) break;
           uint8_t* sa = smem + stage * sh.stage_bytes;
           mbar_expect_tx(&ctl->full[stage], two ? 2 * kABytes : kABytes);
-          tma_load_2d(sa, m0, &ctl->full[stage], kb * KE, y0);
-          if (two) tma_load_2d(sa + kABytes, m1, &ctl->full[stage], kb * KE, y1);
+          tma_load_2d_hint(sa, m0, &ctl->full[stage], kb * KE, y0, policy);
+          if (two) tma_load_2d_hint(sa + kABytes, m1, &ctl->full[stage], kb * KE, y1, policy);
           ++armed;
           if (++stage == stages) stage = 0, phase ^= 1u;
         }
@@ -296,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         fence_after();
         const uint32_t d0 = tmem_base + (uint32_t)(buf * 2 * N), d1 = d0 + (uint32_t)N;
         const bool two = two_blocks(tl);
-        const int nkb = k_blocks(tl), cols = columns(tl);
-        for (int kb = 0; kb < nkb; ++kb) {
+        const int cols = columns(tl);
+        for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
           if (!(ok = wait(&ctl->full[stage], phase))) break;
           fence_after();
           const uint32_t sa = smem_u32(smem + stage * sh.stage_bytes);
@@ -313,15 +368,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             const uint32_t id = idesc_fp8(cols, kb & 3);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {  // 32 codes = 32 bytes
-              mma_fp8(d0, a0 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, sf, sf + 8, (kb | k) != 0);
-              if (two) mma_fp8(d1, a1 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, sf + 4, sf + 8, (kb | k) != 0);
+              mma_fp8(d0, a0 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, sf, sf + 8, ((kb - tl.kb0) | k) != 0);
+              if (two) mma_fp8(d1, a1 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, sf + 4, sf + 8, ((kb - tl.kb0) | k) != 0);
             }
           } else {
             const uint32_t id = idesc_bf16(cols);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {  // 16 bf16 = 32 bytes
-              mma_bf16(d0, a0 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, (kb | k) != 0);
-              if (two) mma_bf16(d1, a1 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, (kb | k) != 0);
+              mma_bf16(d0, a0 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, ((kb - tl.kb0) | k) != 0);
+              if (two) mma_bf16(d1, a1 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, ((kb - tl.kb0) | k) != 0);
             }
           }
           issued = true;
@@ -366,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
       quant_ok = true;
       const bool s = tl.e == a.E;
       const CUtensorMap* m = !tl.down ? &maps.x : (s ? &maps.hs : &maps.h);
-      const int cols = columns(tl), nkb = k_blocks(tl);
+      const int cols = columns(tl), nkb = (tl.down ? tl.Ie : a.d) / KE;  // FP8: scale bytes per row
       // scale bytes: rows of the token operand, and the two weight blocks
       const uint8_t *tok = nullptr, *w0 = nullptr, *w1 = nullptr;
       if constexpr (FP8) {
@@ -391,14 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
       };
       uint32_t wt0 = 0, wt1 = 0, ww0 = 0, ww1 = 0;
       auto fetch = [&](int kb) {  // lane l holds token rows l and l + 32
-        if (kb >= nkb) return;
+        if (kb >= tl.kb1) return;
         wt0 = lane < rows ? word(tok + (int64_t)lane * nkb, kb, true) : 0u;
         wt1 = lane + 32 < rows ? word(tok + (int64_t)(lane + 32) * nkb, kb, true) : 0u;
         ww0 = word(w0, kb, false);
         ww1 = word(w1, kb, false);
       };
-      if constexpr (FP8) fetch(0);
-      for (int kb = 0; kb < nkb; ++kb) {
+      if constexpr (FP8) fetch(tl.kb0);
+      for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
         if (!all(lane != 0 || wait(&ctl->empty[stage], phase ^ 1u))) {
           ok = false;
           break;
@@ -498,20 +553,71 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         fence_after();
         const uint32_t d0 = tmem_base + ((uint32_t)(rw * 32) << 16) + (uint32_t)(buf * 2 * N), d1 = d0 + (uint32_t)N;
         const bool s = tl.e == a.E;
+        auto release = [&] {  // the accumulators are read
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->tmem_empty[buf]);
+        };
+        // what the four warps wrote is visible to whoever sees the count; true for the count's last
+        auto count = [&](int32_t* p, int target) {
+          fence_async_global();  // h is read by TMA
+          __threadfence();
+          named_sync<2, 128>();
+          if (r == 0) ctl->last = add_release(p, 1) + 1 == target;
+          named_sync<2, 128>();
+          return ctl->last != 0;
+        };
         if (!tl.down) {
           const int c = tl.r0 + r;  // hidden column
-          for (int t0 = 0; t0 < N; t0 += 16) {
-            const uint32_t mine = (uint32_t)(tl.mask >> t0) & 0xFFFFu;
+          float* part = a.gu + (s ? (int64_t)a.n * a.k * a.cut.s1 * 2 * a.I : 0);  // [rows, parts, 2, Ie]
+          if (tl.parts > 1) {
+            int row = tl.row0;
+            for (int t0 = 0; t0 < N; t0 += 4) {
+              const uint32_t mine = (uint32_t)(tl.mask >> t0) & 15u;
+              if (!mine) continue;
+              float g[4], u[4];
+              tmem_ld4x2(d0 + (uint32_t)t0, d1 + (uint32_t)t0, g, u);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (!((mine >> j) & 1u)) continue;
+                float* o = part + ((int64_t)row++ * tl.parts + tl.part) * 2 * tl.Ie + c;
+                if (c < tl.Ie) o[0] = g[j], o[tl.Ie] = u[j];
+              }
+            }
+            release();
+            // the block that brings a tile's last part adds the parts, in order, and goes on with the sums
+            if (!count(a.ctr + kCtrExpert + a.E + 1 + (a.d + kMinColumns - 1) / kMinColumns + tl.e * tiles1 + tl.r0 / kRows,
+                       tl.parts))
+              continue;
+          }
+          int row = tl.row0;
+          for (int t0 = 0; t0 < N; t0 += 4) {  // four at a time: more, unrolled, missed the instruction cache
+            const uint32_t mine = (uint32_t)(tl.mask >> t0) & 15u;
             if (!mine) continue;
-            float g[16], u[16];
-            tmem_ld16(d0 + (uint32_t)t0, g);
-            tmem_ld16(d1 + (uint32_t)t0, u);
-            int row = tl.row0 + __popcll(tl.mask & ((1ull << t0) - 1ull));
+            float g[4], u[4];
+            if (tl.parts > 1) {
+              int from = row;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                g[j] = u[j] = 0.0f;
+                if (!((mine >> j) & 1u) || c >= tl.Ie) continue;
+                const float* o = part + (int64_t)from++ * tl.parts * 2 * tl.Ie + c;
+#pragma unroll 4
+                for (int p = 0; p < tl.parts; ++p) {
+                  g[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie);
+                  u[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie + tl.Ie);
+                }
+              }
+            } else {
+              tmem_ld4x2(d0 + (uint32_t)t0, d1 + (uint32_t)t0, g, u);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[j] = silu(g[j]) * u[j];
             if constexpr (FP8) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
+              for (int j = 0; j < 4; ++j) {
                 if (!((mine >> j) & 1u)) continue;
-                g[j] = to_f32(from_f32<bf16>(silu(g[j]) * u[j]));
+                g[j] = to_f32(from_f32<bf16>(g[j]));
                 const float v = fabsf(g[j]);  // a NaN is left out of the maximum
                 const unsigned top = __reduce_max_sync(kFull, v >= 0.0f ? __float_as_uint(v) : 0u);
                 if (lane == 0) reinterpret_cast<float*>(&ctl->amax[j])[rw] = __uint_as_float(top);
@@ -520,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
               uint8_t* hq = static_cast<uint8_t*>(s ? a.hs : a.h);
               uint8_t* hb = s ? a.hs_scale : a.h_scale;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
+              for (int j = 0; j < 4; ++j) {
                 if (!((mine >> j) & 1u)) continue;
                 const float4 m4 = ctl->amax[j];
                 const int e = ue8m0_exponent(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)));
@@ -532,22 +638,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             } else {
               bf16* h = static_cast<bf16*>(s ? a.hs : a.h);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
+              for (int j = 0; j < 4; ++j) {
                 if (!((mine >> j) & 1u)) continue;
-                if (c < tl.Ie) h[(int64_t)row * tl.Ie + c] = from_f32<bf16>(silu(g[j]) * u[j]);
+                if (c < tl.Ie) h[(int64_t)row * tl.Ie + c] = from_f32<bf16>(g[j]);
                 ++row;
               }
             }
           }
-        } else {
-          float* out = s ? a.es : a.eo + (int64_t)tl.row0 * a.d;
+          if (tl.parts == 1) release();
+          count(a.ctr + kCtrExpert + tl.e, INT_MAX);
+          continue;
+        }
+        {
+          const int64_t rows = s ? a.n : (int64_t)a.n * a.k;
+          float* out = (s ? a.es : a.eo) + (tl.part * rows + tl.row0) * a.d;
           const bool two = two_blocks(tl);
-          for (int t0 = 0; t0 < tl.m; t0 += 16) {
-            float v0[16], v1[16];
-            tmem_ld16(d0 + (uint32_t)t0, v0);
-            if (two) tmem_ld16(d1 + (uint32_t)t0, v1);
+          for (int t0 = 0; t0 < tl.m; t0 += 4) {
+            float v0[4], v1[4];
+            tmem_ld4x2(d0 + (uint32_t)t0, (two ? d1 : d0) + (uint32_t)t0, v0, v1);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 4; ++j) {
               if (t0 + j >= tl.m) break;
               float* o = out + (int64_t)(t0 + j) * a.d + tl.r0 + r;
               if (tl.r0 + r < a.d) o[0] = v0[j];
@@ -555,39 +665,35 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             }
           }
         }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->tmem_empty[buf]);
-        fence_async_global();  // h is read by TMA
-        __threadfence();
-        named_sync<2, 128>();
-        if (!tl.down) {
-          if (r == 0) add_release(a.ctr + kCtrExpert + tl.e, 1);
-          continue;
-        }
-        if (r == 0) ctl->last = add_release(a.ctr + kCtrExpert + a.E + 1 + tl.r0 / kColumns, 1) + 1 == ctl->plan.n_act + shared;
-        named_sync<2, 128>();
-        if (!ctl->last) continue;
-        // the last expert's tile of these columns adds them up, in slot order, the shared experts last
-        const int c = tl.r0 + 2 * r;
-        if (c < a.d) {
-          for (int t2 = 0; t2 < a.n; ++t2) {
-            float2 y = make_float2(0.0f, 0.0f);
-            for (int j = 0; j < a.k; ++j) {
-              const int row = slot_r[t2 * a.k + j];
-              if (row == 0xFFFF) continue;
-              const float w = slot_w[t2 * a.k + j];
-              const float2 o = __ldcg(reinterpret_cast<const float2*>(a.eo + (int64_t)row * a.d + c));
-              y.x = fmaf(w, o.x, y.x);
-              y.y = fmaf(w, o.y, y.y);
-            }
-            if (shared) {
-              const float2 o = __ldcg(reinterpret_cast<const float2*>(a.es + (int64_t)t2 * a.d + c));
-              y.x += o.x;
-              y.y += o.y;
-            }
-            reinterpret_cast<__nv_bfloat162*>(static_cast<bf16*>(a.y) + (int64_t)t2 * a.d + c)[0] = __floats2bfloat162_rn(y.x, y.y);
+        release();
+        if (!count(a.ctr + kCtrExpert + a.E + 1 + tl.r0 / kColumns, ctl->plan.n_act * a.cut.s2 + shared * a.cut.s2s)) continue;
+        // the last tile of these columns adds them up: the slots in order, each one's parts in order,
+        // the shared experts last; four columns a thread, two tokens at a time
+        const int c = tl.r0 + 4 * (r & 63);
+        if (c >= a.d) continue;
+        const int64_t nk = (int64_t)a.n * a.k;
+        for (int t2 = r >> 6; t2 < a.n; t2 += 2) {
+          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          auto add = [&](const float* p, float w) {
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(p));
+            y.x = fmaf(w, o.x, y.x);
+            y.y = fmaf(w, o.y, y.y);
+            y.z = fmaf(w, o.z, y.z);
+            y.w = fmaf(w, o.w, y.w);
+          };
+          int j = t2 * a.k, p = 0;
+#pragma unroll 8
+          for (int i2 = 0; i2 < a.k * a.cut.s2; ++i2) {
+            add(a.eo + (p * nk + slot_r[j]) * a.d + c, slot_w[j]);
+            if (++p == a.cut.s2) p = 0, ++j;
           }
+          if (shared) {
+#pragma unroll 4
+            for (p = 0; p < a.cut.s2s; ++p) add(a.es + ((int64_t)p * a.n + t2) * a.d + c, 1.0f);
+          }
+          __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(static_cast<bf16*>(a.y) + (int64_t)t2 * a.d + c);
+          o[0] = __floats2bfloat162_rn(y.x, y.y);
+          o[1] = __floats2bfloat162_rn(y.z, y.w);
         }
       }
     }
@@ -617,16 +723,70 @@ bool make_map(CUtensorMap* m, bool fp8, const void* base, int64_t rows, int64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Zeroes the status block and the counters. The layer's kernel is launched while this one runs
+// (programmatic dependent launch) and sets up its shared and tensor memory meanwhile; its
+// griddepcontrol.wait returns once these stores are visible. A memset node in front of the kernel
+// cost 2 us more per call.
+__global__ void __launch_bounds__(256) clear_kernel(uint4* p, int n) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = threadIdx.x; i < n; i += 256) p[i] = make_uint4(0, 0, 0, 0);
+}
+
+// Launch that may begin before the kernel in front of it has ended; both kernels wait for that end
+// (griddepcontrol.wait) before they touch memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), int grid, int block, size_t smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <bool FP8>
 cudaError_t launch_t(const DecodeArgs& a, const DecodeMaps& maps, const TcShape& sh, int grid, size_t smem, cudaStream_t s) {
   static std::atomic<uint64_t> attr;
   const cudaError_t e = set_smem_limit(attr, (const void*)decode_tc_kernel<FP8>, kSmemLimit);
   if (e != cudaSuccess) return e;
-  decode_tc_kernel<FP8><<<grid, kThreads, smem, s>>>(maps, a, sh);
-  return cudaGetLastError();
+  return launch_early(decode_tc_kernel<FP8>, grid, kThreads, smem, s, maps, a, sh);
+}
+
+// Parts of a k axis of nkb blocks, so that `tiles` tiles of it make about `target`, each of at least
+// kMinPart blocks (FP8: whole words of four scale bytes).
+void split_k(int64_t tiles, int64_t target, int64_t nkb, int32_t* parts, int32_t* per) {
+  int64_t p = ceil_div(target, tiles > 0 ? tiles : 1);
+  if (p > nkb / kMinPart) p = nkb / kMinPart;
+  if (p > kMaxParts) p = kMaxParts;
+  if (p < 1) p = 1;
+  *per = (int32_t)align_up(nkb > 0 ? ceil_div(nkb, p) : 1, 4);
+  *parts = nkb > 0 ? (int32_t)ceil_div(nkb, *per) : 1;
 }
 
 }  // namespace
+
+DecodeSplits decode_splits(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I, int32_t Is, int32_t dtype) {
+  DecodeSplits c{1, 0, 1, 0, 1, 0, 1, 0};
+  if (dtype == MOE_F32) return c;
+  const int64_t ke = dtype == MOE_FP8 ? 128 : 64;
+  const int64_t active = n * k < E ? n * k : E;  // experts at most
+  const int64_t tiles2 = ceil_div(d, kColumns);
+  split_k(active * ceil_div(I, kRows), kTiles1, ceil_div(d, ke), &c.s1, &c.per1);
+  split_k(ceil_div(Is, kRows), kTiles1, ceil_div(d, ke), &c.s1s, &c.per1s);
+  split_k((active + (Is > 0)) * tiles2, kTiles2, ceil_div(I, ke), &c.s2, &c.per2);
+  split_k((active + (Is > 0)) * tiles2, kTiles2, ceil_div(Is, ke), &c.s2s, &c.per2s);
+  return c;
+}
+
+int64_t decode_counters(const DecodeSplits& cut, int32_t d, int32_t E, int32_t I, int32_t Is) {
+  return kCtrExpert + E + 1 + ceil_div(d, kMinColumns) + (cut.s1 > 1 || cut.s1s > 1 ? E * ceil_div(I, kRows) + ceil_div(Is, kRows) : 0);
+}
 
 bool decode_tc_supported(const DecodeArgs& a) {
   const int64_t widest = a.I > a.d ? a.I : a.d;
@@ -661,6 +821,8 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s) {
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (sms <= 0) sms = 148;
+  const cudaError_t e = launch_early(clear_kernel, 1, 256, 0, s, reinterpret_cast<uint4*>(a.clear), a.clear_bytes / 16);
+  if (e != cudaSuccess) return e;
   return fp8 ? launch_t<true>(a, m, sh, sms, smem, s) : launch_t<false>(a, m, sh, sms, smem, s);
 }
 

@@ -175,7 +175,14 @@ cudaError_t launch_refine(const RouteTcArgs& a, cudaStream_t s);
 
 // The whole layer for n <= MOE_DECODE_MAX_TOKENS tokens in one launch (decode.cuh has the scheme).
 // act: float (MOE_F32) or bf16; FP8 experts read x and h as E4M3 codes with UE8M0 bytes per 1 x 128.
+// How the tensor-core form cuts the k axis of its tiles (decode_tc.cu): parts, and 128-byte k blocks
+// per part, of the gate/up (1) and down (2) tiles of the routed and of the shared (s) experts.
+struct DecodeSplits {
+  int32_t s1, per1, s1s, per1s, s2, per2, s2s, per2s;
+};
+DecodeSplits decode_splits(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I, int32_t Is, int32_t dtype);
 struct DecodeArgs {
+  DecodeSplits cut;
   int32_t n, d, E, k, G, topk_group, score_fn, renorm, I, Is, dtype;
   float rsf;
   const void* x;             // [n, d]
@@ -193,15 +200,18 @@ struct DecodeArgs {
   void* hs;                  // [n, Is]
   uint8_t* h_scale;          // FP8: [n * k, I / 128]
   uint8_t* hs_scale;         // FP8: [n, Is / 128]
-  float* eo;                 // [n * k, d] expert outputs, rows by expert then token
-  float* es;                 // [n, d] shared experts' output
+  float* gu;                 // tiles in parts: [n * k, s1, 2, I] gate and up sums, then [n, s1s, 2, Is]
+  float* eo;                 // [s2, n * k, d] expert outputs, rows by expert then token
+  float* es;                 // [s2s, n, d] shared experts' output
   void* y;                   // [n, d]
   int32_t* counts;           // [E] or nullptr
   moe_diag* diag;            // or nullptr
-  int32_t* ctr;              // counters, zeroed before the launch
+  int32_t* ctr;              // counters
+  void* clear;               // the status block and the counters: zeroed in front of the kernel
+  int32_t clear_bytes;
   moe_diag* status;
 };
-int64_t decode_counters(int32_t E, int32_t d);  // counter words
+int64_t decode_counters(const DecodeSplits& cut, int32_t d, int32_t E, int32_t I, int32_t Is);  // counter words
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s);  // bf16 and FP8 experts
 bool decode_tc_supported(const DecodeArgs& a);
