@@ -272,7 +272,8 @@ __device__ __noinline__ double block_reduce(double v, double* part, int tid, Syn
 // an expert each: an expert's place is the number of better keys, counted over shared memory, first
 // in its warp, then for each warp's k best among those of all. `bias` is the thread's expert's. One
 // warp walking top-k rounds with eight experts a lane took 49 us at E = 256: its code does not fit
-// the instruction cache, and a block runs it once.
+// the instruction cache, and a block runs it once. The counts are free of branches: with a short-
+// circuit the lanes of a tie test ran one by one.
 template <typename Sync>
 __device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScratch* sc, int tid, Sync sync) {
   const int e = tid;
@@ -292,9 +293,10 @@ __device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScrat
     const int per = a.E / a.G, g = e / per;
     if (live) {
       int better = 0;
+#pragma unroll 4
       for (int f = g * per; f < (g + 1) * per; ++f) {
         const unsigned long long o = sc->key[f];
-        better += o > key || (o == key && f < e);
+        better += (o > key) | ((o == key) & (f < e));
       }
       if (better < 2) sc->best[better][g] = sel;
       if (per == 1) sc->best[1][g] = -INFINITY;
@@ -305,7 +307,7 @@ __device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScrat
     if (live) {
       const unsigned long long mine = sc->group[g];
       int better = 0;
-      for (int h = 0; h < a.G; ++h) better += sc->group[h] > mine || (sc->group[h] == mine && h < g);
+      for (int h = 0; h < a.G; ++h) better += (sc->group[h] > mine) | ((sc->group[h] == mine) & (h < g));
       if (better >= a.topk_group) sc->key[e] = key = 0ull;
     }
     sync();
@@ -313,7 +315,8 @@ __device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScrat
   if (a.score_fn == MOE_SCORE_SOFTMAX) {
     const double m = block_reduce<false>(live ? l : -INFINITY, sc->part, tid, sync);
     score = live ? exp(l - m) : 0.0;
-    score /= block_reduce<true>(score, sc->part, tid, sync);
+    const double z = block_reduce<true>(score, sc->part, tid, sync);
+    if (live) score /= z;  // (a quotient of 0 takes the division's slow path, ten times as long)
   }
   {
     const int w0 = tid & ~31, per_warp = min(a.k, 32);
@@ -322,7 +325,7 @@ __device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScrat
 #pragma unroll 8
       for (int f = 0; f < 32; ++f) {
         const unsigned long long o = sc->key[w0 + f];
-        better += o > key || (o == key && w0 + f < e);
+        better += (o > key) | ((o == key) & (w0 + f < e));
       }
     } else {
       better = tid & 31;
@@ -338,7 +341,7 @@ __device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScrat
 #pragma unroll 8
       for (int f = 0; f < count; ++f) {
         const unsigned long long o = sc->top[f];
-        better += o > key || (o == key && sc->top_e[f] < e);
+        better += (o > key) | ((o == key) & (sc->top_e[f] < e));
       }
       if (better < a.k) {
         sc->idx[better] = e;
@@ -352,7 +355,7 @@ __device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScrat
     const double denom = a.renorm ? warp_sum(v) : 1.0;
     if (tid < a.k) {
       a.topk_idx[t * a.k + tid] = sc->idx[tid];
-      a.topk_w[t * a.k + tid] = (float)(v / denom * (double)a.rsf);
+      a.topk_w[t * a.k + tid] = (float)(v / denom * (double)a.rsf);  // lanes with a slot only, as above
     }
   }
   sync();

@@ -158,8 +158,10 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* m
 // Orders generic writes before, and async-proxy (TMA) reads after, across the release/acquire pair between them.
 __device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
+// Barrier of COUNT threads. bar.sync wants whole warps: lanes that left a loop apart meet first.
 template <int ID, int COUNT>
 __device__ __forceinline__ void named_sync() {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(COUNT) : "memory");
 }
 
@@ -184,6 +186,7 @@ __device__ __forceinline__ void tmem_ld4x2(uint32_t a0, uint32_t a1, float (&v0)
 template <int ID, int COUNT>
 __device__ __forceinline__ bool named_and(bool v) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %1, 0;\n\t"
