@@ -1027,6 +1027,7 @@ moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, con
   if (tensor && !decode_tc_supported(a)) return MOE_ERR_UNSUPPORTED;
   a.clear = c.ws;
   a.clear_bytes = (int32_t)align_up((int64_t)c.p.dctr + decode_counters(a.cut, a.d, a.E, a.I, a.Is) * 4, 16);
+  MOE_CUDA(launch_decode_router(a, c.s));
   return cuda_status(tensor ? launch_decode_tc(a, c.s) : launch_decode_simt(a, c.s));
 }
 

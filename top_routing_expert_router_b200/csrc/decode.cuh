@@ -1,13 +1,15 @@
-// decode.cuh -- what the one-kernel layers for few tokens share (decode_simt.cu, decode_tc.cu):
-// arguments, the counters that order the work inside the launch, the router in binary64, the plan
-// of active experts and the combine.
+// decode.cuh -- what the layers for few tokens share (decode_router.cu, decode_simt.cu,
+// decode_tc.cu): the counters that order the work inside a launch, the routing decision, the plan of
+// active experts.
 //
-// The layer of n <= 64 tokens is one launch. Its work is cut into units that thread blocks claim
-// from counters in the workspace, in this order: E4M3 rows of x (FP8), router logits, routing
-// decisions, gate/up tiles (shared experts first), down tiles. A unit waits only for units that
-// were claimed before it, so some block is running each of them and every wait ends, whatever
-// share of the grid is resident: no cooperative launch, and calls on several streams may overlap
-// on the GPU. Waits are bounded all the same (kDecodeTimeoutNs).
+// The layer of n <= 64 tokens is two launches. The first (decode_router.cu) computes the router
+// logits, quantises x where the experts want E4M3, and clears the counters; the second is set up
+// meanwhile (programmatic dependent launch) and does the rest. Its work is cut into units that
+// thread blocks claim from counters in the workspace, in this order: routing decisions, gate/up
+// tiles (shared experts first), down tiles. A unit waits only for units that were claimed before
+// it, so some block is running each of them and every wait ends, whatever share of the grid is
+// resident: no cooperative launch, and calls on several streams may overlap on the GPU. Waits are
+// bounded all the same (kDecodeTimeoutNs).
 //
 // Sums are deterministic: no floating-point atomics; the block that finishes the last down tile of
 // a column range adds that range's expert rows in slot order.
@@ -27,17 +29,16 @@ constexpr uint64_t kDecodeTimeoutNs = 2000000000ull;  // 2 s for any single wait
 // Counter words (zeroed before the launch).
 enum {
   kCtrAbort = 0,
-  kCtrQuant,       // E4M3 rows handed out / finished
-  kCtrQuantDone,
-  kCtrLogit,       // router units
-  kCtrLogitDone,
-  kCtrToken,       // routing decisions, a block each
+  kCtrToken,       // routing decisions handed out / finished
   kCtrTokenDone,
-  kCtrTile,        // gate/up and down tiles
+  kCtrTile,        // gate/up and down tiles handed out
   kCtrExpert = 16  // [E + 1] finished gate/up tiles per expert (E: shared), then [column ranges] finished down
                    // tiles, then (gate/up tiles cut along k) [E * tiles + shared tiles] finished parts
 };
 constexpr int kMinColumns = 32;  // output columns of a down tile, at least
+// Up to here every block decides the tokens itself: a decision takes 1.5 us, handing it on through
+// global memory as long again.
+constexpr int kSelfTokens = 2;
 
 __device__ __forceinline__ int ld_acquire(const int32_t* p) {
   int v;
@@ -80,18 +81,6 @@ __device__ __forceinline__ uint32_t quantize_tile(const float (&v)[4], uint32_t*
   return e4m3x4(v[0], v[1], v[2], v[3], pow2_neg(e));
 }
 
-// Tile i of x's n * d / 128 (row by row), by one warp.
-__device__ __forceinline__ void quantize_x_tile(const DecodeArgs& a, int64_t i) {
-  const int lane = threadIdx.x & 31;
-  const uint2 raw = __ldg(reinterpret_cast<const uint2*>(a.x) + i * 32 + lane);
-  const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u), __uint_as_float(raw.y << 16),
-                      __uint_as_float(raw.y & 0xFFFF0000u)};
-  uint32_t byte;
-  const uint32_t q = quantize_tile(v, &byte);
-  reinterpret_cast<uint32_t*>(a.xq)[i * 32 + lane] = q;
-  if (lane == 0) a.xs[i] = (uint8_t)byte;
-}
-
 // ---- router ------------------------------------------------------------------------
 
 // 16 bytes of activations or router weights as binary32 (8 bf16 or 4 binary32 values).
@@ -111,125 +100,10 @@ __device__ __forceinline__ void unpack(const uint4& raw, float (&v)[4]) {
   v[0] = __uint_as_float(raw.x), v[1] = __uint_as_float(raw.y), v[2] = __uint_as_float(raw.z), v[3] = __uint_as_float(raw.w);
 }
 
-// Experts per router unit: the units spread over the grid.
-__host__ __device__ inline int router_unit(int E, int grid) { return (E + grid - 1) / grid; }
-
-// A binary32 value times 2^-896 as a binary64, exact for every finite value (subnormals and zeros
-// included: the fields only move): three integer operations, where the conversion instruction runs
-// at 4 lanes a clock and SM and made the logits of 64 tokens take 150 us.
-__device__ __forceinline__ double widened(float v) {
-  const int u = __float_as_int(v);
-  return __hiloint2double((u >> 3) & (int)0x8FFFFFFF, u << 29);
-}
-// A router weight gets 2^512 (two steps: 2^(896 + 512) is past the range), so that its products with
-// widened activations are 2^-384 of the true ones, far from both ends of the range.
-__device__ __forceinline__ double widened_weight(float v) { return widened(v) * 0x1p1000 * 0x1p408; }
-constexpr double kWidenLogit = 0x1p384;
-
-constexpr int kRouterTokens = 4;  // tokens of one dot-product item: each weight is widened once for them
-
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
   return v;
-}
-
-// Binary64 logits of experts e0 and (pair) e0 + 1 for every token, by the NW warps of a block (warp
-// `w`; `part`: NW * 2 * kRouterTokens doubles). Products of bf16 values are exact, sums are binary64.
-// Items are groups of TOK tokens, cut along d when there are fewer of them than warps; a cut item's
-// parts are added in order. The loads of BATCH steps are issued before their products: a step whose
-// loads wait on branches took a memory latency per token. A row with a NaN or an infinity gets NaN
-// logits (the widening alone would take them for finite values). `sync` is a barrier of these warps.
-template <typename T, int NW, int TOK, int BATCH, typename Sync>
-__device__ void router_logits_pair(const DecodeArgs& a, int e0, bool pair, int w, double* part, Sync sync) {
-  constexpr int C = Chunk<T>::N;
-  const int lane = threadIdx.x & 31;
-  const int items = (a.n + TOK - 1) / TOK;
-  const int cuts = items >= NW ? 1 : NW / items;
-  const int chunks = a.d / C;  // d % 8 == 0
-  const int per = (chunks + cuts - 1) / cuts;
-  const uint4* w0 = reinterpret_cast<const uint4*>(static_cast<const T*>(a.w_router) + (int64_t)e0 * a.d);
-  const uint4* w1 = pair ? w0 + chunks : w0;
-  for (int it = w; it < items * cuts; it += NW) {
-    const int item = it / cuts, cut = it % cuts, t0 = item * TOK;
-    const int last = min(TOK, a.n - t0) - 1;
-    const uint4* xr = reinterpret_cast<const uint4*>(a.x) + (int64_t)t0 * chunks;
-    double acc[2][TOK] = {};
-    float odd[2] = {}, odd_x[TOK] = {};  // NaN once a value is not finite
-    const int c1 = min(chunks, (cut + 1) * per);
-    for (int c0 = cut * per; c0 < c1; c0 += 32 * BATCH) {
-      uint4 r0[BATCH], r1[BATCH], rx[BATCH][TOK];
-#pragma unroll
-      for (int b = 0; b < BATCH; ++b) {
-        const int c = c0 + 32 * b + lane;
-        const bool in = c < c1;
-        r0[b] = in ? __ldg(w0 + c) : make_uint4(0, 0, 0, 0);
-        r1[b] = in ? __ldg(w1 + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int q = 0; q < TOK; ++q)  // past the last token: its row again, not stored
-          rx[b][q] = in ? __ldg(xr + (int64_t)min(q, last) * chunks + c) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int b = 0; b < BATCH; ++b) {
-        float v0[C], v1[C];
-        unpack(r0[b], v0);
-        unpack(r1[b], v1);
-        double d0[C], d1[C];
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-          d0[j] = widened_weight(v0[j]);
-          d1[j] = widened_weight(v1[j]);
-          odd[0] = fmaf(v0[j], 0.0f, odd[0]);
-          odd[1] = fmaf(v1[j], 0.0f, odd[1]);
-        }
-#pragma unroll
-        for (int q = 0; q < TOK; ++q) {
-          float xv[C];
-          unpack(rx[b][q], xv);
-#pragma unroll
-          for (int j = 0; j < C; ++j) {
-            const double xd = widened(xv[j]);
-            acc[0][q] = fma(xd, d0[j], acc[0][q]);
-            acc[1][q] = fma(xd, d1[j], acc[1][q]);
-            odd_x[q] = fmaf(xv[j], 0.0f, odd_x[q]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < TOK; ++q)
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const double s = warp_sum(acc[p][q] * kWidenLogit + (double)(odd[p] + odd_x[q]));
-        if (lane != 0 || (p && !pair) || q > last) continue;
-        if (cuts == 1)
-          a.logits[(int64_t)(t0 + q) * a.E + e0 + p] = s;
-        else
-          part[(it * 2 + p) * TOK + q] = s;  // it < items * cuts <= NW
-      }
-  }
-  if (cuts == 1) return;
-  sync();
-  if (w == 0)
-    for (int i = lane; i < items * 2 * TOK; i += 32) {
-      const int item = i / (2 * TOK), p = i / TOK % 2, q = i % TOK;
-      const int t = item * TOK + q;
-      if (t >= a.n || (p && !pair)) continue;
-      double s = 0.0;
-      for (int cut = 0; cut < cuts; ++cut) s += part[((item * cuts + cut) * 2 + p) * TOK + q];
-      a.logits[(int64_t)t * a.E + e0 + p] = s;
-    }
-  sync();  // `part` is the next pair's
-}
-
-template <typename T, int NW, typename Sync>
-__device__ void router_logits_unit(const DecodeArgs& a, int e0, int e1, int w, double* part, Sync sync) {
-  for (int e = e0; e < e1; e += 2) {
-    if (a.n == 1)
-      router_logits_pair<T, NW, 1, 4>(a, e, e + 1 < e1, w, part, sync);
-    else
-      router_logits_pair<T, NW, kRouterTokens, 2>(a, e, e + 1 < e1, w, part, sync);
-  }
 }
 
 // Order-preserving key of a double: a larger value has a larger key; never 0. -0 is taken as +0
@@ -241,9 +115,11 @@ __device__ __forceinline__ unsigned long long order_key(double v) {
 }
 
 struct __align__(16) DecideScratch {
-  unsigned long long key[kMaxExperts];  // selection values; 0: not eligible
-  unsigned long long top[kMaxExperts];  // each warp's k best keys and experts, best first
-  int16_t top_e[kMaxExperts];
+  uint32_t hi[kMaxExperts];             // upper halves of the selection keys; 0: not eligible
+  unsigned long long top[kMaxExperts];  // each warp's k best keys, best first (0: none)
+  int16_t top_e[kMaxExperts];           // and their experts
+  uint8_t place[kMaxExperts];           // an expert's slot
+  unsigned long long key[kMaxExperts];
   unsigned long long group[kMaxGroups];
   double best[2][kMaxGroups];
   double part[8];
@@ -268,15 +144,16 @@ __device__ __noinline__ double block_reduce(double v, double* part, int tid, Syn
   return v;
 }
 
-// Token t's experts and gates from its binary64 logits (definitions in router.cu), by 256 threads,
-// an expert each: an expert's place is the number of better keys, counted over shared memory, first
-// in its warp, then for each warp's k best among those of all. `bias` is the thread's expert's. One
-// warp walking top-k rounds with eight experts a lane took 49 us at E = 256: its code does not fit
-// the instruction cache, and a block runs it once. The counts are free of branches: with a short-
-// circuit the lanes of a tie test ran one by one.
+// Token t's experts and gates from its binary64 logits (definitions in router.cu) to out_idx and
+// out_w, by 256 threads, an expert each; `bias` is the thread's expert's.
+// An expert's place is the number of better ones: first in its warp, by the upper halves of the keys
+// (a warp with two equal halves counts the whole keys), then each warp's k best among those of all.
+// Counting costs 1.5 us at E = 256, top-8 of 4 of 8 groups. One warp walking top-k rounds with eight
+// experts a lane took 49 us (its code, run once, comes from memory), counting whole keys 3.6 us.
 template <typename Sync>
-__device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScratch* sc, int tid, Sync sync) {
-  const int e = tid;
+__device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScratch* sc, int tid, Sync sync, int* out_idx,
+                             float* out_w) {
+  const int e = tid, lane = tid & 31, w0 = tid & ~31;
   const bool live = e < a.E;
   const double l = live ? __ldcg(a.logits + (int64_t)t * a.E + e) : 0.0;
   double score = l;  // what the gate is made of
@@ -287,75 +164,108 @@ __device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScrat
   const double sel = score + (double)bias;
   unsigned long long key = live ? order_key(sel) : 0ull;
   sc->key[e] = key;
-  sync();
+  sc->place[e] = 0xFF;
   if (a.G > 1) {
     // the two best of each group, then the groups by their sum (ties: the lower group)
     const int per = a.E / a.G, g = e / per;
-    if (live) {
-      int better = 0;
-#pragma unroll 4
-      for (int f = g * per; f < (g + 1) * per; ++f) {
-        const unsigned long long o = sc->key[f];
-        better += (o > key) | ((o == key) & (f < e));
+    if (per == 32) {  // a group is a warp
+      if (live) {
+        const unsigned hi = (unsigned)(key >> 32), lo = (unsigned)key;
+        const unsigned h1 = __reduce_max_sync(kFull, hi), l1 = __reduce_max_sync(kFull, hi == h1 ? lo : 0u);
+        const int first = __ffs(__ballot_sync(kFull, hi == h1 && lo == l1)) - 1;
+        const unsigned hr = lane == first ? 0u : hi;
+        const unsigned h2 = __reduce_max_sync(kFull, hr), l2 = __reduce_max_sync(kFull, hr == h2 ? lo : 0u);
+        const int second = __ffs(__ballot_sync(kFull, hr == h2 && lo == l2)) - 1;
+        const double b = __shfl_sync(kFull, sel, first) + __shfl_sync(kFull, sel, second);
+        if (lane == 0) sc->group[g] = order_key(b);
       }
-      if (better < 2) sc->best[better][g] = sel;
-      if (per == 1) sc->best[1][g] = -INFINITY;
+    } else {
+      sync();
+      if (live) {
+        int better = 0;
+#pragma unroll 4
+        for (int f = g * per; f < (g + 1) * per; ++f) {
+          const unsigned long long o = sc->key[f];
+          better += (o > key) | ((o == key) & (f < e));
+        }
+        if (better < 2) sc->best[better][g] = sel;
+        if (per == 1) sc->best[1][g] = -INFINITY;
+      }
+      sync();
+      if (tid < a.G) sc->group[tid] = order_key(sc->best[0][tid] + sc->best[1][tid]);
     }
-    sync();
-    if (tid < a.G) sc->group[tid] = order_key(sc->best[0][tid] + sc->best[1][tid]);
     sync();
     if (live) {
       const unsigned long long mine = sc->group[g];
       int better = 0;
+#pragma unroll 8
       for (int h = 0; h < a.G; ++h) better += (sc->group[h] > mine) | ((sc->group[h] == mine) & (h < g));
       if (better >= a.topk_group) sc->key[e] = key = 0ull;
     }
-    sync();
   }
+  sc->hi[e] = (uint32_t)(key >> 32);
   if (a.score_fn == MOE_SCORE_SOFTMAX) {
     const double m = block_reduce<false>(live ? l : -INFINITY, sc->part, tid, sync);
     score = live ? exp(l - m) : 0.0;
-    const double z = block_reduce<true>(score, sc->part, tid, sync);
-    if (live) score /= z;  // (a quotient of 0 takes the division's slow path, ten times as long)
+    score /= block_reduce<true>(score, sc->part, tid, sync);
   }
-  {
-    const int w0 = tid & ~31, per_warp = min(a.k, 32);
-    int better = 0;
-    if (w0 < a.E) {
-#pragma unroll 8
+  const int per_warp = min(a.k, 32);
+  if (w0 < a.E) {
+    unsigned long long* top = sc->top + (w0 >> 5) * per_warp;
+    if (lane < per_warp) top[lane] = 0ull;
+    __syncwarp();  // the warp's keys and empty list
+    const uint32_t mine = (uint32_t)(key >> 32);
+    int better = 0, same = 0;
+#pragma unroll
+    for (int f = 0; f < 32; f += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(sc->hi + w0 + f);
+      better += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+      same += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
+    }
+    if (__any_sync(kFull, key && same > 1)) {
+      better = 0;
       for (int f = 0; f < 32; ++f) {
         const unsigned long long o = sc->key[w0 + f];
-        better += (o > key) | ((o == key) & (w0 + f < e));
+        better += (o > key) | ((o == key) & (f < lane));
       }
-    } else {
-      better = tid & 31;
     }
-    if (better < per_warp) {  // experts past E and groups left out come last, with key 0
-      sc->top[(w0 >> 5) * per_warp + better] = key;
+    if (key && better < per_warp) {
+      top[better] = key;
       sc->top_e[(w0 >> 5) * per_warp + better] = (int16_t)e;
     }
-    sync();
-    if (key && better < per_warp) {
-      const int count = (a.E + 31) / 32 * per_warp;
-      better = 0;
-#pragma unroll 8
-      for (int f = 0; f < count; ++f) {
+  }
+  sync();
+  // every candidate against the others, four lanes a candidate
+  const int count = (a.E + 31) / 32 * per_warp;
+  for (int c0 = 0; c0 < count; c0 += 64) {
+    const int c = c0 + (tid >> 2);
+    const unsigned long long mine = c < count ? sc->top[c] : 0ull;
+    const int ce = mine ? sc->top_e[c] : 0;
+    int better = 0;
+    if (mine) {
+#pragma unroll 4
+      for (int f = tid & 3; f < count; f += 4) {
         const unsigned long long o = sc->top[f];
-        better += (o > key) | ((o == key) & (sc->top_e[f] < e));
-      }
-      if (better < a.k) {
-        sc->idx[better] = e;
-        sc->val[better] = score;
+        better += (o > mine) | ((o == mine) & (sc->top_e[f] < ce));
       }
     }
+    better += __shfl_xor_sync(kFull, better, 1);
+    better += __shfl_xor_sync(kFull, better, 2);
+    if (mine && (tid & 3) == 0 && better < a.k) sc->place[ce] = (uint8_t)better;
+  }
+  sync();
+  const int slot = sc->place[e];
+  if (slot < a.k) {
+    sc->idx[slot] = e;
+    sc->val[slot] = score;
   }
   sync();
   if (tid < 32) {
     const double v = tid < a.k ? sc->val[tid] : 0.0;
     const double denom = a.renorm ? warp_sum(v) : 1.0;
     if (tid < a.k) {
-      a.topk_idx[t * a.k + tid] = sc->idx[tid];
-      a.topk_w[t * a.k + tid] = (float)(v / denom * (double)a.rsf);  // lanes with a slot only, as above
+      out_idx[tid] = sc->idx[tid];
+      out_w[tid] = (float)(v / denom * (double)a.rsf);
     }
   }
   sync();
@@ -379,18 +289,19 @@ __device__ __forceinline__ int slot_row(const DecodePlan& p, int e, int t) {
   return p.off[e] + __popcll(p.mask[e] & ((1ull << t) - 1ull));
 }
 
-// Built by NT threads (tid 0 .. NT-1, warp 0 among them) from the finished decisions; slot_w and
-// slot_r (given: [n * k]) receive each slot's gate and its row. The masks are zero.
+// Built by NT threads (tid 0 .. NT-1, warp 0 among them) from the finished decisions at idx and w;
+// slot_w and slot_r (given: [n * k]) receive each slot's gate and its row. The masks are zero.
 template <int NT, typename Sync>
-__device__ void build_plan(const DecodeArgs& a, DecodePlan* p, float* slot_w, uint16_t* slot_r, int tid, Sync sync) {
+__device__ void build_plan(const DecodeArgs& a, const int* idx, const float* w, DecodePlan* p, float* slot_w,
+                           uint16_t* slot_r, int tid, Sync sync) {
   const int slots = a.n * a.k;
+  // idx and w: global memory written in this launch (never through L1), or shared memory
+  const volatile int* vi = idx;
+  const volatile float* vw = w;
   // the first NT slots stay in registers: most batches have no more
-  const int e0 = tid < slots ? __ldcg(a.topk_idx + tid) : -1;
-  const float g0 = tid < slots ? __ldcg(a.topk_w + tid) : 0.0f;
-  for (int s = tid; s < slots; s += NT) {
-    const int e = s == tid ? e0 : __ldcg(a.topk_idx + s);
-    atomicOr(&p->mask[e], 1ull << (s / a.k));
-  }
+  const int e0 = tid < slots ? vi[tid] : 0;
+  const float g0 = tid < slots ? vw[tid] : 0.0f;
+  for (int s = tid; s < slots; s += NT) atomicOr(&p->mask[s == tid ? e0 : vi[s]], 1ull << (s / a.k));
   sync();
   if (tid < 32) {
     constexpr int PER = kMaxExperts / 32;
@@ -422,9 +333,8 @@ __device__ void build_plan(const DecodeArgs& a, DecodePlan* p, float* slot_w, ui
   sync();
   if (slot_w)
     for (int s = tid; s < slots; s += NT) {
-      const int e = s == tid ? e0 : __ldcg(a.topk_idx + s);
-      slot_w[s] = s == tid ? g0 : __ldcg(a.topk_w + s);
-      slot_r[s] = (uint16_t)slot_row(*p, e, s / a.k);
+      slot_w[s] = s == tid ? g0 : vw[s];
+      slot_r[s] = (uint16_t)slot_row(*p, s == tid ? e0 : vi[s], s / a.k);
     }
 }
 
@@ -446,6 +356,24 @@ __device__ void write_counts(const DecodeArgs& a, const DecodePlan& p, int tid) 
     }
   }
 }
+
+// Launch that may begin before the kernel in front of it has ended; every kernel launched so waits
+// for that end (griddepcontrol.wait) before it touches global memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), int grid, int block, size_t smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace
 }  // namespace moe

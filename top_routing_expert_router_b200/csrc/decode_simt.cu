@@ -1,5 +1,4 @@
-// decode_simt.cu -- the one-kernel layer for few tokens on the CUDA cores (decode.cuh has the
-// scheme and the router).
+// decode_simt.cu -- the layer for few tokens on the CUDA cores: binary32 (decode.cuh has the scheme).
 //
 //   h[r, i]  = silu(x_t . gate_e[i]) * (x_t . up_e[i])   for slot row r of token t, expert e
 //   o[r, c]  = h[r] . down_e[c],   y[t] = sum_j w_tj o[row(t, j)] + shared(x_t)
@@ -40,9 +39,12 @@ struct Types<MOE_FP8> {
 
 struct Shared {
   DecodePlan plan;
+  float slot_w[MOE_DECODE_MAX_TOKENS * kMaxTopK];
+  uint16_t slot_r[MOE_DECODE_MAX_TOKENS * kMaxTopK];
+  int32_t sel_e[kSelfTokens * kMaxTopK];
+  float sel_w[kSelfTokens * kMaxTopK];
   union {
     DecideScratch decide;
-    double part[kWarps * 2 * kRouterTokens];
     float h[MOE_DECODE_MAX_TOKENS][128];
   };
   uint8_t tok[MOE_DECODE_MAX_TOKENS];
@@ -125,28 +127,24 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
     __syncthreads();
     return sm.ok != 0;
   };
-  const int quant = DT == MOE_FP8 && a.quantize ? a.n * (a.d / 128) : 0;  // tiles of x
-  const int quants = (quant + kWarps - 1) / kWarps;
-  for (int u; quant && (u = claim(kCtrQuant)) < quants;) {
-    if (u * kWarps + warp < quant) quantize_x_tile(a, u * kWarps + warp);
-    finish(a.ctr + kCtrQuantDone);
-  }
+  wait_for_earlier_kernels();
   const Act* x = DT == MOE_FP8 ? reinterpret_cast<const Act*>(a.xq) : static_cast<const Act*>(a.x);
-  const int unit = router_unit(a.E, gridDim.x), units = (a.E + unit - 1) / unit;
-  for (int u; (u = claim(kCtrLogit)) < units;) {
-    router_logits_unit<Out, kWarps>(a, u * unit, min(a.E, (u + 1) * unit), warp, sm.part, sync);
-    finish(a.ctr + kCtrLogitDone);
-  }
-  for (int e = tid; e < kMaxExperts; e += kThreads) sm.plan.mask[e] = 0ull;
+  sm.plan.mask[tid] = 0ull;
   const float bias = a.bias && tid < a.E ? __ldg(a.bias + tid) : 0.0f;
-  for (int t; (t = claim(kCtrToken)) < a.n;) {
-    if (!wait(a.ctr + kCtrLogitDone, units)) return;
-    decide_token(a, t, bias, &sm.decide, tid, sync);
-    finish(a.ctr + kCtrTokenDone);
+  const bool self = a.n <= kSelfTokens;
+  if (self) {
+    for (int t = 0; t < a.n; ++t)
+      decide_token(a, t, bias, &sm.decide, tid, sync, sm.sel_e + t * a.k, sm.sel_w + t * a.k);
+    if (blockIdx.x == 0)
+      for (int s = tid; s < a.n * a.k; s += kThreads) a.topk_idx[s] = sm.sel_e[s], a.topk_w[s] = sm.sel_w[s];
+  } else {
+    for (int t; (t = claim(kCtrToken)) < a.n;) {
+      decide_token(a, t, bias, &sm.decide, tid, sync, a.topk_idx + t * a.k, a.topk_w + t * a.k);
+      finish(a.ctr + kCtrTokenDone);
+    }
+    if (!wait(a.ctr + kCtrTokenDone, a.n)) return;
   }
-  if (!wait(a.ctr + kCtrTokenDone, a.n)) return;
-  if (quant && !wait(a.ctr + kCtrQuantDone, quants)) return;
-  build_plan<kThreads>(a, &sm.plan, nullptr, nullptr, tid, sync);
+  build_plan<kThreads>(a, self ? sm.sel_e : a.topk_idx, self ? sm.sel_w : a.topk_w, &sm.plan, sm.slot_w, sm.slot_r, tid, sync);
   if (blockIdx.x == 0) write_counts<kThreads>(a, sm.plan, tid);
 
   const int shared = a.Is > 0;
@@ -243,8 +241,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
       if (c >= i1) continue;
       float s = 0.0f;
       for (int j = 0; j < a.k; ++j) {
-        const int ej = __ldcg(a.topk_idx + t2 * a.k + j);
-        s = fmaf(__ldcg(a.topk_w + t2 * a.k + j), __ldcg(a.eo + (int64_t)slot_row(sm.plan, ej, t2) * a.d + c), s);
+        s = fmaf(sm.slot_w[t2 * a.k + j], __ldcg(a.eo + (int64_t)sm.slot_r[t2 * a.k + j] * a.d + c), s);
       }
       if (shared) s += __ldcg(a.es + (int64_t)t2 * a.d + c);
       static_cast<Out*>(a.y)[(int64_t)t2 * a.d + c] = from_f32<Out>(s);
@@ -255,12 +252,9 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
 template <int DT>
 cudaError_t launch_t(const DecodeArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> attr;
-  cudaError_t e = set_smem_limit(attr, (const void*)decode_simt_kernel<DT>, sizeof(Shared));
+  const cudaError_t e = set_smem_limit(attr, (const void*)decode_simt_kernel<DT>, sizeof(Shared));
   if (e != cudaSuccess) return e;
-  e = cudaMemsetAsync(a.clear, 0, (size_t)a.clear_bytes, s);
-  if (e != cudaSuccess) return e;
-  decode_simt_kernel<DT><<<148 * 2, kThreads, sizeof(Shared), s>>>(a);
-  return cudaGetLastError();
+  return launch_early(decode_simt_kernel<DT>, 148 * 2, kThreads, sizeof(Shared), s, a);
 }
 
 }  // namespace

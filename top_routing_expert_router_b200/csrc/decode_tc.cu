@@ -1,5 +1,5 @@
-// decode_tc.cu -- the one-kernel layer for few tokens on the tcgen05 tensor cores (bf16 and FP8
-// experts; decode.cuh has the scheme and the router).
+// decode_tc.cu -- the layer for few tokens on the tcgen05 tensor cores: bf16 and FP8 experts
+// (decode.cuh has the scheme).
 //
 // The weights are the M side: a tile is two blocks of 128 weight rows (gate and up rows of the same
 // 128 hidden columns; 256 output columns of a down matrix) times N token columns, N = the tokens
@@ -15,12 +15,12 @@
 //   warp 2      copies the token operand of each stage (x, or h once its expert's gate/up tiles are
 //               finished) and, for FP8, writes the stage's scale words.
 //   warp 1      owns TMEM and issues the MMAs; tcgen05.commit frees stages.
-//   warps 4-7   router, then the epilogue: SwiGLU and h (FP8: its E4M3 tile, whose 128 columns are
+//   warps 4-7   routing decisions and the plan, then the epilogue: SwiGLU and h (FP8: its E4M3 tile, whose 128 columns are
 //               the tile's 128 lanes), or the down tile's rows and, after a column range's last
 //               tile, the combine.
-//   warps 8-11  router.
-// The shared experts' tiles need no routing and come first, so the weights stream while the router
-// runs. FP8 scales ride in the MMA (kind::mxf8f6f4.block_scale): one scale word holds four 128-wide
+//   warps 8-11  routing decisions and the plan.
+// The shared experts' tiles need no routing and come first, so the weights stream while tokens are
+// decided. FP8 scales ride in the MMA (kind::mxf8f6f4.block_scale): one scale word holds four 128-wide
 // k blocks, so every fourth stage carries scale words, copied into TMEM by tcgen05.cp.
 #include <cuda.h>
 #include <limits.h>
@@ -70,7 +70,8 @@ struct __align__(16) Ctl {
   int32_t routed;              // every token's decision was seen
   int32_t last;
   float4 amax[16];             // FP8: a column's largest |h| per epilogue warp
-  double part[kRouterWarps * 2 * kRouterTokens];
+  int32_t sel_e[kSelfTokens * kMaxTopK];  // the block's own decisions
+  float sel_w[kSelfTokens * kMaxTopK];
   DecideScratch decide;
   DecodePlan plan;
 };
@@ -83,7 +84,8 @@ struct TcShape {
   int32_t n_cols;       // token columns: n rounded up to 16
   int32_t stages;
   int32_t stage_bytes;
-  int32_t slot_off;     // bytes from the ring to the combine's slots
+  int32_t sf_off;       // bytes from the ring to the stages' scale words (FP8)
+  int32_t slot_off;     // to the combine's slots
   int32_t ctl_off;
 };
 
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
   __syncthreads();
   fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero, earlier kernels' writes visible
+  wait_for_earlier_kernels();
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_try(smem_u32(bar), parity) || mbar_wait(bar, parity, ctl, a.ctr, a.status);
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
           if constexpr (FP8) {
             const uint32_t sf = tmem_base + kSfCol0 + kSfCols * (uint32_t)((kb >> 2) & 1);
             if ((kb & 3) == 0) {
-              const uint32_t ss = sa + 2 * kABytes + (uint32_t)N * kKB;
+              const uint32_t ss = smem_u32(smem + sh.sf_off + stage * 3 * kSfBytes);
               sf_copy(sf, sf_desc(ss));
               sf_copy(sf + 4, sf_desc(ss + kSfBytes));
               sf_copy(sf + 8, sf_desc(ss + 2 * kSfBytes));
@@ -398,8 +400,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     // ================= tokens (and FP8 scale words) =================
     int stage = 0, q = 0;
     uint32_t phase = 0, qphase = 0;
-    bool quant_ok = !(FP8 && a.quantize);
-    const int quants = (a.n * (a.d / 128) + kRouterWarps - 1) / kRouterWarps;
     auto all = [&](bool v) { return __shfl_sync(kFull, (int)v, 0) != 0; };
     for (;;) {
       if (!all(lane != 0 || wait(&ctl->tile_full[q], qphase))) break;
@@ -410,18 +410,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->tile_empty[q]);
       if (++q == kQueue) q = 0, qphase ^= 1u;
-      // what this tile reads is written: x's codes, or h of its expert
       bool ok = true;
       if (lane == 0) {
-        if (tl.down)
-          ok = wait_counter(a.ctr + kCtrExpert + tl.e, tl.e == a.E ? tiles1s : tiles1, a.ctr, a.status);
-        else if (!quant_ok)
-          ok = wait_counter(a.ctr + kCtrQuantDone, quants, a.ctr, a.status);
+        if (tl.down) ok = wait_counter(a.ctr + kCtrExpert + tl.e, tl.e == a.E ? tiles1s : tiles1, a.ctr, a.status);  // its h
         fence_async_global();
         if (!ok) atomicExch(&ctl->abort, 1);
       }
       if (!all(ok)) break;
-      quant_ok = true;
       const bool s = tl.e == a.E;
       const CUtensorMap* m = !tl.down ? &maps.x : (s ? &maps.hs : &maps.h);
       const int cols = columns(tl), nkb = (tl.down ? tl.Ie : a.d) / KE;  // FP8: scale bytes per row
@@ -463,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
         uint8_t* sb = smem + stage * sh.stage_bytes + 2 * kABytes;
         if (FP8 && (kb & 3) == 0) {
-          uint4* sf = reinterpret_cast<uint4*>(sb + N * kKB);
+          uint4* sf = reinterpret_cast<uint4*>(smem + sh.sf_off + stage * 3 * kSfBytes);
           sf[lane] = make_uint4(ww0, ww0, ww0, ww0);
           sf[32 + lane] = make_uint4(ww1, ww1, ww1, ww1);
           sf[64 + lane] = make_uint4(wt0, wt1, 0u, 0u);
@@ -486,53 +481,35 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     // ================= router =================
     const int tid = threadIdx.x - 128, rw = warp - 4;
     auto sync = [] { named_sync<1, kRouterThreads>(); };
-    const int quants = FP8 && a.quantize ? (a.n * (a.d / 128) + kRouterWarps - 1) / kRouterWarps : 0;
-    const int unit = router_unit(a.E, gridDim.x), units = (a.E + unit - 1) / unit;
     ctl->plan.mask[tid] = 0ull;
     const float bias = a.bias && tid < a.E ? __ldg(a.bias + tid) : 0.0f;
-    for (;;) {  // E4M3 tiles of x, then logits
-      if (tid == 0) ctl->ticket = atomicAdd(a.ctr + kCtrLogit, 1);
-      sync();
-      const int u = ctl->ticket;
-      if (u >= quants + units) break;
-      if (u < quants) {
-        const int i = u * kRouterWarps + rw;
-        if (i < a.n * (a.d / 128)) quantize_x_tile(a, i);
-        fence_async_global();  // the codes are read by TMA
-      } else {
-        const int e0 = (u - quants) * unit;
-        router_logits_unit<bf16, kRouterWarps>(a, e0, min(a.E, e0 + unit), rw, ctl->part, sync);
-      }
-      __threadfence();
-      sync();
-      if (tid == 0) add_release(a.ctr + (u < quants ? kCtrQuantDone : kCtrLogitDone), 1);
-    }
-    sync();  // everyone has read the last ticket
+    const bool self = a.n <= kSelfTokens;
     bool ok = true;
-    auto all_ok = [&](bool v) {  // thread 0's answer for all: the barriers count every router warp
-      if (tid == 0) ctl->routed = v;
-      sync();
-      return ctl->routed != 0;
-    };
-    for (;;) {
-      if (tid == 0) {
-        ctl->ticket = atomicAdd(a.ctr + kCtrToken, 1);
-        if (ctl->ticket < a.n) ok = wait_counter(a.ctr + kCtrLogitDone, units, a.ctr, a.status);
+    if (self) {
+      for (int t = 0; t < a.n; ++t)
+        decide_token(a, t, bias, &ctl->decide, tid, sync, ctl->sel_e + t * a.k, ctl->sel_w + t * a.k);
+      if (blockIdx.x == 0 && tid < a.n * a.k) a.topk_idx[tid] = ctl->sel_e[tid], a.topk_w[tid] = ctl->sel_w[tid];
+    } else {
+      for (;;) {
+        if (tid == 0) ctl->ticket = atomicAdd(a.ctr + kCtrToken, 1);
+        sync();
+        const int t = ctl->ticket;
+        if (t >= a.n) break;
+        decide_token(a, t, bias, &ctl->decide, tid, sync, a.topk_idx + t * a.k, a.topk_w + t * a.k);
+        __threadfence();
+        sync();
+        if (tid == 0) add_release(a.ctr + kCtrTokenDone, 1);
       }
-      ok = all_ok(ok);
-      const int t = ctl->ticket;
-      if (!ok || t >= a.n) break;
-      decide_token(a, t, bias, &ctl->decide, tid, sync);
-      __threadfence();
+      if (tid == 0) {
+        ctl->routed = wait_counter(a.ctr + kCtrTokenDone, a.n, a.ctr, a.status);
+        if (!ctl->routed) atomicExch(&ctl->abort, 1);
+      }
       sync();
-      if (tid == 0) add_release(a.ctr + kCtrTokenDone, 1);
+      ok = ctl->routed != 0;  // one answer for all: the barriers below count every router warp
     }
-    if (tid == 0 && ok) ok = wait_counter(a.ctr + kCtrTokenDone, a.n, a.ctr, a.status);
-    if (tid == 0 && !ok) atomicExch(&ctl->abort, 1);
-    sync();  // everyone has read the last answer
-    ok = all_ok(ok);
     if (ok) {
-      build_plan<kRouterThreads>(a, &ctl->plan, slot_w, slot_r, tid, sync);
+      build_plan<kRouterThreads>(a, self ? ctl->sel_e : a.topk_idx, self ? ctl->sel_w : a.topk_w, &ctl->plan, slot_w, slot_r, tid,
+                                 sync);
       sync();
       if (lane == 0) mbar_arrive(&ctl->plan_ready);
       if (blockIdx.x == 0 && rw >= 4) write_counts<kRouterThreads - 128>(a, ctl->plan, tid - 128);
@@ -726,33 +703,6 @@ bool make_map(CUtensorMap* m, bool fp8, const void* base, int64_t rows, int64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Zeroes the status block and the counters. The layer's kernel is launched while this one runs
-// (programmatic dependent launch) and sets up its shared and tensor memory meanwhile; its
-// griddepcontrol.wait returns once these stores are visible. A memset node in front of the kernel
-// cost 2 us more per call.
-__global__ void __launch_bounds__(256) clear_kernel(uint4* p, int n) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int i = threadIdx.x; i < n; i += 256) p[i] = make_uint4(0, 0, 0, 0);
-}
-
-// Launch that may begin before the kernel in front of it has ended; both kernels wait for that end
-// (griddepcontrol.wait) before they touch memory.
-template <typename... Params, typename... Args>
-cudaError_t launch_early(void (*kernel)(Params...), int grid, int block, size_t smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <bool FP8>
 cudaError_t launch_t(const DecodeArgs& a, const DecodeMaps& maps, const TcShape& sh, int grid, size_t smem, cudaStream_t s) {
   static std::atomic<uint64_t> attr;
@@ -800,11 +750,13 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s) {
   const bool fp8 = a.dtype == MOE_FP8;
   TcShape sh{};
   sh.n_cols = (int32_t)align_up(a.n, 16);
-  sh.stage_bytes = 2 * kABytes + sh.n_cols * kKB + (fp8 ? (int32_t)align_up(3 * kSfBytes, 1024) : 0);
+  sh.stage_bytes = 2 * kABytes + sh.n_cols * kKB;
   const int64_t slots = align_up((int64_t)a.n * a.k * 6, 16);
-  const int64_t fit = ((int64_t)kSmemLimit - 1024 - slots - (int64_t)sizeof(Ctl)) / sh.stage_bytes;
+  const int64_t sf = fp8 ? 3 * kSfBytes : 0;  // scale words, outside the stages to keep those on 1024 bytes
+  const int64_t fit = ((int64_t)kSmemLimit - 1024 - slots - (int64_t)sizeof(Ctl)) / (sh.stage_bytes + sf);
   sh.stages = (int32_t)(fit < kMaxStages ? fit : kMaxStages);
-  sh.slot_off = sh.stages * sh.stage_bytes;
+  sh.sf_off = sh.stages * sh.stage_bytes;
+  sh.slot_off = sh.sf_off + sh.stages * (int32_t)sf;
   sh.ctl_off = sh.slot_off + (int32_t)slots;
   const size_t smem = 1024 + (size_t)sh.ctl_off + sizeof(Ctl);
   if (sh.stages < 2) return cudaErrorInvalidValue;
@@ -824,8 +776,6 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s) {
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (sms <= 0) sms = 148;
-  const cudaError_t e = launch_early(clear_kernel, 1, 256, 0, s, reinterpret_cast<uint4*>(a.clear), a.clear_bytes / 16);
-  if (e != cudaSuccess) return e;
   return fp8 ? launch_t<true>(a, m, sh, sms, smem, s) : launch_t<false>(a, m, sh, sms, smem, s);
 }
 

@@ -173,7 +173,7 @@ cudaError_t launch_route_tc(const RouteTcArgs& a, cudaStream_t s);
 // d (bf16 rows, d % 8 == 0, 16-byte aligned), queue, cand, cand_val, pairs and pair_count.
 cudaError_t launch_refine(const RouteTcArgs& a, cudaStream_t s);
 
-// The whole layer for n <= MOE_DECODE_MAX_TOKENS tokens in one launch (decode.cuh has the scheme).
+// The whole layer for n <= MOE_DECODE_MAX_TOKENS tokens in two launches (decode.cuh has the scheme).
 // act: float (MOE_F32) or bf16; FP8 experts read x and h as E4M3 codes with UE8M0 bytes per 1 x 128.
 // How the tensor-core form cuts the k axis of its tiles (decode_tc.cu): parts, and 128-byte k blocks
 // per part, of the gate/up (1) and down (2) tiles of the routed and of the shared (s) experts.
@@ -207,13 +207,14 @@ struct DecodeArgs {
   int32_t* counts;           // [E] or nullptr
   moe_diag* diag;            // or nullptr
   int32_t* ctr;              // counters
-  void* clear;               // the status block and the counters: zeroed in front of the kernel
+  void* clear;               // the status block and the counters: zeroed by the first launch
   int32_t clear_bytes;
   moe_diag* status;
 };
 int64_t decode_counters(const DecodeSplits& cut, int32_t d, int32_t E, int32_t I, int32_t Is);  // counter words
-cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t s);
-cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s);  // bf16 and FP8 experts
+cudaError_t launch_decode_router(const DecodeArgs& a, cudaStream_t s);  // first: logits, x's codes, cleared counters
+cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t s);    // then the layer: binary32,
+cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s);      // or bf16 and FP8 experts
 bool decode_tc_supported(const DecodeArgs& a);
 
 // Capacity rule over the ranking on many SMs (capacity.cu): a cooperative grid, one token per
