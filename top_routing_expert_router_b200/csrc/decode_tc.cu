@@ -496,9 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         const int t = ctl->ticket;
         if (t >= a.n) break;
         decide_token(a, t, bias, &ctl->decide, tid, sync, a.topk_idx + t * a.k, a.topk_w + t * a.k);
-        __threadfence();
-        sync();
-        if (tid == 0) add_release(a.ctr + kCtrTokenDone, 1);
+        if (tid == 0) add_release(a.ctr + kCtrTokenDone, 1);  // decide_token ends with a barrier
       }
       if (tid == 0) {
         ctl->routed = wait_counter(a.ctr + kCtrTokenDone, a.n, a.ctr, a.status);
@@ -538,10 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->tmem_empty[buf]);
         };
-        // what the four warps wrote is visible to whoever sees the count; true for the count's last
+        // what the four warps wrote is visible to whoever sees the count (the barrier puts it before
+        // thread 0's release, which is cumulative; a fence in every thread cost 2 us a call); true for
+        // the count's last
         auto count = [&](int32_t* p, int target) {
           fence_async_global();  // h is read by TMA
-          __threadfence();
           named_sync<2, 128>();
           if (r == 0) ctl->last = add_release(p, 1) + 1 == target;
           named_sync<2, 128>();
