@@ -11,8 +11,8 @@
 // resident: no cooperative launch, and calls on several streams may overlap on the GPU. Waits are
 // bounded all the same (kDecodeTimeoutNs).
 //
-// Sums are deterministic: no floating-point atomics; the block that finishes the last down tile of
-// a column range adds that range's expert rows in slot order.
+// Sums are deterministic: no floating-point atomics; whichever block adds the expert rows of a
+// column range takes them in slot order.
 #pragma once
 
 #include "common.cuh"

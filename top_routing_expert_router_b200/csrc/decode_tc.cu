@@ -16,8 +16,7 @@
 //               finished) and, for FP8, writes the stage's scale words.
 //   warp 1      owns TMEM and issues the MMAs; tcgen05.commit frees stages.
 //   warps 4-7   routing decisions and the plan, then the epilogue: SwiGLU and h (FP8: its E4M3 tile, whose 128 columns are
-//               the tile's 128 lanes), or the down tile's rows and, after a column range's last
-//               tile, the combine.
+//               the tile's 128 lanes) or the down tile's rows, and at last the combine.
 //   warps 8-11  routing decisions and the plan.
 // The shared experts' tiles need no routing and come first, so the weights stream while tokens are
 // decided. FP8 scales ride in the MMA (kind::mxf8f6f4.block_scale): one scale word holds four 128-wide
@@ -40,6 +39,7 @@ constexpr int kKB = 128;                    // bytes of k per stage and row
 constexpr int kABytes = kRows * kKB;        // one weight block
 constexpr int kSfBytes = 512;
 constexpr int kColumns = 2 * kRows;         // output columns of a down tile
+constexpr int kCombineTokens = 8;           // tokens of a combine unit
 constexpr int kMaxStages = 8;
 constexpr int kQueue = 4;                   // tiles published ahead of the slowest reader
 constexpr uint32_t kTmemCols = 512;
@@ -517,162 +517,198 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
       const int r = rw * 32 + lane;  // weight row of the tile: TMEM lane (quarter rw = warp % 4)
       int q = 0, i = 0;
       uint32_t qphase = 0;
-      for (;; ++i) {
-        const int buf = i & 1;
-        bool go = wait(&ctl->tile_full[q], qphase);
-        const int t = go ? *reinterpret_cast<volatile int32_t*>(&ctl->tile[q]) : 0;
-        if (go && t >= 0) go = wait(&ctl->tmem_full[buf], (uint32_t)(i >> 1) & 1u);
-        // one answer for the four warps: the barriers below count all of them
-        if (!named_and<2, 128>(go) || t < 0) break;
-        const Tile tl = tile_of(t);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->tile_empty[q]);
-        if (++q == kQueue) q = 0, qphase ^= 1u;
-        fence_after();
-        const uint32_t d0 = tmem_base + ((uint32_t)(rw * 32) << 16) + (uint32_t)(buf * 2 * N), d1 = d0 + (uint32_t)N;
-        const bool s = tl.e == a.E;
-        auto release = [&] {  // the accumulators are read
-          fence_before();
+      // Combine: y of 256 columns and eight tokens a unit: each slot's parts in order, the slots in order,
+      // the shared experts last. Four columns a thread, two tokens at once. For a few tokens the block
+      // that finishes a column range adds it at once (Mixtral shapes n=1: 132 us a call, 133.4 otherwise); for
+      // more, the units are spread over the blocks after their tiles (nobody waits for a unit, so each
+      // block has its own): with one block adding all tokens of a range, 64 tokens took 28 SMs about 30 us
+      // after the last weight had arrived.
+      const bool few = a.n <= 4;
+      const int chunks = (a.n + kCombineTokens - 1) / kCombineTokens;
+      const int parts = ctl->plan.n_act * a.cut.s2 + shared * a.cut.s2s;  // down tiles of a column range
+      bool tiles_left = true;
+      int unit = few ? INT_MAX : (int)blockIdx.x;
+      for (;;) {
+        int u;
+        if (tiles_left) {
+          const int buf = i & 1;
+          bool go = wait(&ctl->tile_full[q], qphase);
+          const int t = go ? *reinterpret_cast<volatile int32_t*>(&ctl->tile[q]) : 0;
+          if (go && t >= 0) go = wait(&ctl->tmem_full[buf], (uint32_t)(i >> 1) & 1u);
+          // one answer for the four warps: the barriers below count all of them
+          if (!named_and<2, 128>(go)) break;
+          if (t < 0) {
+            tiles_left = false;
+            continue;
+          }
+          ++i;
+          const Tile tl = tile_of(t);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->tmem_empty[buf]);
-        };
-        // what the four warps wrote is visible to whoever sees the count (the barrier puts it before
-        // thread 0's release, which is cumulative; a fence in every thread cost 2 us a call); true for
-        // the count's last
-        auto count = [&](int32_t* p, int target) {
-          fence_async_global();  // h is read by TMA
-          named_sync<2, 128>();
-          if (r == 0) ctl->last = add_release(p, 1) + 1 == target;
-          named_sync<2, 128>();
-          return ctl->last != 0;
-        };
-        if (!tl.down) {
-          const int c = tl.r0 + r;  // hidden column
-          float* part = a.gu + (s ? (int64_t)a.n * a.k * a.cut.s1 * 2 * a.I : 0);  // [rows, parts, 2, Ie]
-          if (tl.parts > 1) {
+          if (lane == 0) mbar_arrive(&ctl->tile_empty[q]);
+          if (++q == kQueue) q = 0, qphase ^= 1u;
+          fence_after();
+          const uint32_t d0 = tmem_base + ((uint32_t)(rw * 32) << 16) + (uint32_t)(buf * 2 * N), d1 = d0 + (uint32_t)N;
+          const bool s = tl.e == a.E;
+          auto release = [&] {  // the accumulators are read
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->tmem_empty[buf]);
+          };
+          // what the four warps wrote is visible to whoever sees the count (the barrier puts it before
+          // thread 0's release, which is cumulative; a fence in every thread cost 2 us a call); true for
+          // the count's last
+          auto count = [&](int32_t* p, int target) {
+            fence_async_global();  // h is read by TMA
+            named_sync<2, 128>();
+            if (r == 0) ctl->last = add_release(p, 1) + 1 == target;
+            named_sync<2, 128>();
+            return ctl->last != 0;
+          };
+          if (!tl.down) {
+            const int c = tl.r0 + r;  // hidden column
+            float* part = a.gu + (s ? (int64_t)a.n * a.k * a.cut.s1 * 2 * a.I : 0);  // [rows, parts, 2, Ie]
+            if (tl.parts > 1) {
+              int row = tl.row0;
+              for (int t0 = 0; t0 < N; t0 += 4) {
+                const uint32_t mine = (uint32_t)(tl.mask >> t0) & 15u;
+                if (!mine) continue;
+                float g[4], u[4];
+                tmem_ld4x2(d0 + (uint32_t)t0, d1 + (uint32_t)t0, g, u);
+  #pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if (!((mine >> j) & 1u)) continue;
+                  float* o = part + ((int64_t)row++ * tl.parts + tl.part) * 2 * tl.Ie + c;
+                  if (c < tl.Ie) o[0] = g[j], o[tl.Ie] = u[j];
+                }
+              }
+              release();
+              // the block that brings a tile's last part adds the parts, in order, and goes on with the sums
+              if (!count(a.ctr + kCtrExpert + a.E + 1 + (a.d + kMinColumns - 1) / kMinColumns + tl.e * tiles1 + tl.r0 / kRows,
+                         tl.parts))
+                continue;
+            }
             int row = tl.row0;
-            for (int t0 = 0; t0 < N; t0 += 4) {
+            for (int t0 = 0; t0 < N; t0 += 4) {  // four at a time: more, unrolled, missed the instruction cache
               const uint32_t mine = (uint32_t)(tl.mask >> t0) & 15u;
               if (!mine) continue;
               float g[4], u[4];
-              tmem_ld4x2(d0 + (uint32_t)t0, d1 + (uint32_t)t0, g, u);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (!((mine >> j) & 1u)) continue;
-                float* o = part + ((int64_t)row++ * tl.parts + tl.part) * 2 * tl.Ie + c;
-                if (c < tl.Ie) o[0] = g[j], o[tl.Ie] = u[j];
+              if (tl.parts > 1) {
+                int from = row;
+  #pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  g[j] = u[j] = 0.0f;
+                  if (!((mine >> j) & 1u) || c >= tl.Ie) continue;
+                  const float* o = part + (int64_t)from++ * tl.parts * 2 * tl.Ie + c;
+  #pragma unroll 4
+                  for (int p = 0; p < tl.parts; ++p) {
+                    g[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie);
+                    u[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie + tl.Ie);
+                  }
+                }
+              } else {
+                tmem_ld4x2(d0 + (uint32_t)t0, d1 + (uint32_t)t0, g, u);
               }
-            }
-            release();
-            // the block that brings a tile's last part adds the parts, in order, and goes on with the sums
-            if (!count(a.ctr + kCtrExpert + a.E + 1 + (a.d + kMinColumns - 1) / kMinColumns + tl.e * tiles1 + tl.r0 / kRows,
-                       tl.parts))
-              continue;
-          }
-          int row = tl.row0;
-          for (int t0 = 0; t0 < N; t0 += 4) {  // four at a time: more, unrolled, missed the instruction cache
-            const uint32_t mine = (uint32_t)(tl.mask >> t0) & 15u;
-            if (!mine) continue;
-            float g[4], u[4];
-            if (tl.parts > 1) {
-              int from = row;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                g[j] = u[j] = 0.0f;
-                if (!((mine >> j) & 1u) || c >= tl.Ie) continue;
-                const float* o = part + (int64_t)from++ * tl.parts * 2 * tl.Ie + c;
-#pragma unroll 4
-                for (int p = 0; p < tl.parts; ++p) {
-                  g[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie);
-                  u[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie + tl.Ie);
+  #pragma unroll
+              for (int j = 0; j < 4; ++j) g[j] = silu(g[j]) * u[j];
+              if constexpr (FP8) {
+  #pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if (!((mine >> j) & 1u)) continue;
+                  g[j] = to_f32(from_f32<bf16>(g[j]));
+                  const float v = fabsf(g[j]);  // a NaN is left out of the maximum
+                  const unsigned top = __reduce_max_sync(kFull, v >= 0.0f ? __float_as_uint(v) : 0u);
+                  if (lane == 0) reinterpret_cast<float*>(&ctl->amax[j])[rw] = __uint_as_float(top);
+                }
+                named_sync<2, 128>();
+                uint8_t* hq = static_cast<uint8_t*>(s ? a.hs : a.h);
+                uint8_t* hb = s ? a.hs_scale : a.h_scale;
+  #pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if (!((mine >> j) & 1u)) continue;
+                  const float4 m4 = ctl->amax[j];
+                  const int e = ue8m0_exponent(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)));
+                  hq[(int64_t)row * tl.Ie + c] = (uint8_t)__nv_cvt_float_to_fp8(g[j] * pow2_neg(e), __NV_SATFINITE, __NV_E4M3);
+                  if (r == 0) hb[(int64_t)row * (tl.Ie / 128) + tl.r0 / 128] = (uint8_t)(e + 127);
+                  ++row;
+                }
+                named_sync<2, 128>();  // amax is the next columns'
+              } else {
+                bf16* h = static_cast<bf16*>(s ? a.hs : a.h);
+  #pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if (!((mine >> j) & 1u)) continue;
+                  if (c < tl.Ie) h[(int64_t)row * tl.Ie + c] = from_f32<bf16>(g[j]);
+                  ++row;
                 }
               }
-            } else {
-              tmem_ld4x2(d0 + (uint32_t)t0, d1 + (uint32_t)t0, g, u);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) g[j] = silu(g[j]) * u[j];
-            if constexpr (FP8) {
-#pragma unroll
+            if (tl.parts == 1) release();
+            count(a.ctr + kCtrExpert + tl.e, INT_MAX);
+            continue;
+          }
+          {
+            const int64_t rows = s ? a.n : (int64_t)a.n * a.k;
+            float* out = (s ? a.es : a.eo) + (tl.part * rows + tl.row0) * a.d;
+            const bool two = two_blocks(tl);
+            for (int t0 = 0; t0 < tl.m; t0 += 4) {
+              float v0[4], v1[4];
+              tmem_ld4x2(d0 + (uint32_t)t0, (two ? d1 : d0) + (uint32_t)t0, v0, v1);
+  #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                if (!((mine >> j) & 1u)) continue;
-                g[j] = to_f32(from_f32<bf16>(g[j]));
-                const float v = fabsf(g[j]);  // a NaN is left out of the maximum
-                const unsigned top = __reduce_max_sync(kFull, v >= 0.0f ? __float_as_uint(v) : 0u);
-                if (lane == 0) reinterpret_cast<float*>(&ctl->amax[j])[rw] = __uint_as_float(top);
-              }
-              named_sync<2, 128>();
-              uint8_t* hq = static_cast<uint8_t*>(s ? a.hs : a.h);
-              uint8_t* hb = s ? a.hs_scale : a.h_scale;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (!((mine >> j) & 1u)) continue;
-                const float4 m4 = ctl->amax[j];
-                const int e = ue8m0_exponent(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)));
-                hq[(int64_t)row * tl.Ie + c] = (uint8_t)__nv_cvt_float_to_fp8(g[j] * pow2_neg(e), __NV_SATFINITE, __NV_E4M3);
-                if (r == 0) hb[(int64_t)row * (tl.Ie / 128) + tl.r0 / 128] = (uint8_t)(e + 127);
-                ++row;
-              }
-              named_sync<2, 128>();  // amax is the next columns'
-            } else {
-              bf16* h = static_cast<bf16*>(s ? a.hs : a.h);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (!((mine >> j) & 1u)) continue;
-                if (c < tl.Ie) h[(int64_t)row * tl.Ie + c] = from_f32<bf16>(g[j]);
-                ++row;
+                if (t0 + j >= tl.m) break;
+                float* o = out + (int64_t)(t0 + j) * a.d + tl.r0 + r;
+                if (tl.r0 + r < a.d) o[0] = v0[j];
+                if (tl.r0 + kRows + r < a.d) o[kRows] = v1[j];
               }
             }
           }
-          if (tl.parts == 1) release();
-          count(a.ctr + kCtrExpert + tl.e, INT_MAX);
-          continue;
+          release();
+          if (!count(a.ctr + kCtrExpert + a.E + 1 + tl.r0 / kColumns, parts) || !few) continue;
+          u = tl.r0 / kColumns;
+        } else {
+          if (unit >= tiles2 * chunks) break;
+          u = unit;
+          unit += gridDim.x;
+          bool done = true;
+          if (r == 0) done = wait_counter(a.ctr + kCtrExpert + a.E + 1 + u % tiles2, parts, a.ctr, a.status);
+          if (!named_and<2, 128>(done)) break;
         }
-        {
-          const int64_t rows = s ? a.n : (int64_t)a.n * a.k;
-          float* out = (s ? a.es : a.eo) + (tl.part * rows + tl.row0) * a.d;
-          const bool two = two_blocks(tl);
-          for (int t0 = 0; t0 < tl.m; t0 += 4) {
-            float v0[4], v1[4];
-            tmem_ld4x2(d0 + (uint32_t)t0, (two ? d1 : d0) + (uint32_t)t0, v0, v1);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (t0 + j >= tl.m) break;
-              float* o = out + (int64_t)(t0 + j) * a.d + tl.r0 + r;
-              if (tl.r0 + r < a.d) o[0] = v0[j];
-              if (tl.r0 + kRows + r < a.d) o[kRows] = v1[j];
-            }
-          }
-        }
-        release();
-        if (!count(a.ctr + kCtrExpert + a.E + 1 + tl.r0 / kColumns, ctl->plan.n_act * a.cut.s2 + shared * a.cut.s2s)) continue;
-        // the last tile of these columns adds them up: the slots in order, each one's parts in order,
-        // the shared experts last; four columns a thread, two tokens at a time
-        const int c = tl.r0 + 4 * (r & 63);
+        const int c = u % tiles2 * kColumns + 4 * (r & 63);
         if (c >= a.d) continue;
         const int64_t nk = (int64_t)a.n * a.k;
-        for (int t2 = r >> 6; t2 < a.n; t2 += 2) {
-          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          auto add = [&](const float* p, float w) {
+        const int first = u / tiles2 * kCombineTokens, end = min(a.n, first + kCombineTokens);
+        for (int ta = first + (r >> 6); ta < end; ta += 4) {
+          const int tb = ta + 2;
+          const bool two = tb < end;
+          float4 ya = make_float4(0.0f, 0.0f, 0.0f, 0.0f), yb = ya;
+          auto add = [&](float4& y, const float* p, float w) {
             const float4 o = __ldcg(reinterpret_cast<const float4*>(p));
             y.x = fmaf(w, o.x, y.x);
             y.y = fmaf(w, o.y, y.y);
             y.z = fmaf(w, o.z, y.z);
             y.w = fmaf(w, o.w, y.w);
           };
-          int j = t2 * a.k, p = 0;
+          int j = 0, p = 0;
 #pragma unroll 8
           for (int i2 = 0; i2 < a.k * a.cut.s2; ++i2) {
-            add(a.eo + (p * nk + slot_r[j]) * a.d + c, slot_w[j]);
+            add(ya, a.eo + (p * nk + slot_r[ta * a.k + j]) * a.d + c, slot_w[ta * a.k + j]);
+            if (two) add(yb, a.eo + (p * nk + slot_r[tb * a.k + j]) * a.d + c, slot_w[tb * a.k + j]);
             if (++p == a.cut.s2) p = 0, ++j;
           }
           if (shared) {
 #pragma unroll 4
-            for (p = 0; p < a.cut.s2s; ++p) add(a.es + ((int64_t)p * a.n + t2) * a.d + c, 1.0f);
+            for (p = 0; p < a.cut.s2s; ++p) {
+              add(ya, a.es + ((int64_t)p * a.n + ta) * a.d + c, 1.0f);
+              if (two) add(yb, a.es + ((int64_t)p * a.n + tb) * a.d + c, 1.0f);
+            }
           }
-          __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(static_cast<bf16*>(a.y) + (int64_t)t2 * a.d + c);
-          o[0] = __floats2bfloat162_rn(y.x, y.y);
-          o[1] = __floats2bfloat162_rn(y.z, y.w);
+          auto store = [&](int t, const float4& y) {
+            __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(static_cast<bf16*>(a.y) + (int64_t)t * a.d + c);
+            o[0] = __floats2bfloat162_rn(y.x, y.y);
+            o[1] = __floats2bfloat162_rn(y.z, y.w);
+          };
+          store(ta, ya);
+          if (two) store(tb, yb);
         }
       }
     }
