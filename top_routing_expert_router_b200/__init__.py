@@ -210,20 +210,19 @@ def moe_layer_decode(cfg, n, x, weights, y, ws, topk_idx=None, topk_w=None, coun
     """moe_layer_forward for n <= MOE_DECODE_MAX_TOKENS tokens in one launch; x_codes and x_scale_bytes are x's E4M3
     tiles (MOE_FP8) when the caller has them. Every tensor is contiguous and on ws's device."""
     where = "moe_layer_decode"
-    dev, d, slots = ws.device, cfg.d_model, 4 * n * cfg.top_k
+    index, d, slots = ws.get_device(), cfg.d_model, 4 * n * cfg.top_k
     row = n * d * (4 if cfg.dtype == MOE_F32 else 2)
-    for name, t, need in (("x", x, row), ("y", y, row), ("topk_idx", topk_idx, slots), ("topk_w", topk_w, slots),
-                          ("counts", counts, 4 * cfg.n_routed), ("diag", diag, 32), ("x_codes", x_codes, n * d),
-                          ("x_scale_bytes", x_scale_bytes, n * (d // 128)), ("ws", ws, 0)):
+    for t, need in ((x, row), (y, row), (topk_idx, slots), (topk_w, slots), (counts, 4 * cfg.n_routed), (diag, 32),
+                    (x_codes, n * d), (x_scale_bytes, n * (d // 128)), (ws, 0)):
         if t is None:
             continue
-        if t.device != dev or dev.type != "cuda":
+        if index < 0 or t.get_device() != index:
             raise ValueError(f"{where}: every tensor must be on the same CUDA device")
         if t.nbytes < need or not t.is_contiguous():
-            raise ValueError(f"{where}: {name} must be contiguous with at least {need} bytes")
-    _call_on(dev.index, _lib.moe_layer_decode, where, ctypes.byref(cfg), n, _ptr(x), _ptr(x_codes), _ptr(x_scale_bytes),
-             ctypes.byref(weights), _ptr(y), _ptr(topk_idx), _ptr(topk_w), _ptr(counts), _ptr(diag), ws.data_ptr(),
-             ws.nbytes, stream=stream)
+            raise ValueError(f"{where}: a tensor of {t.nbytes} bytes where {need} contiguous ones are needed")
+    _call_on(index, _lib.moe_layer_decode, where,
+             (ctypes.byref(cfg), n, _ptr(x), _ptr(x_codes), _ptr(x_scale_bytes), ctypes.byref(weights), _ptr(y), _ptr(topk_idx),
+              _ptr(topk_w), _ptr(counts), _ptr(diag), ws.data_ptr(), ws.nbytes), stream)
 
 
 def moe_quantize_fp8(x, codes, scale_bytes, stream=None):
@@ -233,15 +232,17 @@ def moe_quantize_fp8(x, codes, scale_bytes, stream=None):
            "moe_quantize_fp8")
 
 
-def _call_on(index, fn, where, *args, stream=None):
-    """fn(*args, stream) with device `index` current; the stream is the device's current one unless given."""
-    import torch
+def _call_on(index, fn, where, args, stream):
+    """fn(*args, stream) with device `index` current; the stream is that device's current one unless given."""
+    from torch import _C, cuda
 
-    if torch.cuda.current_device() == index:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+    if stream is None:
+        stream = _C._cuda_getCurrentRawStream(index)
+    if _C._cuda_getDevice() == index:
+        st = fn(*args, stream)
     else:
-        with torch.cuda.device(index):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+        with cuda.device(index):
+            st = fn(*args, stream)
     if st != MOE_OK:
         raise MoeError(st, where)
 
@@ -254,32 +255,37 @@ def moe_add_rmsnorm(x, weight, eps, y=None, residual=None, sum_out=None, codes=N
     import torch
 
     where = "moe_add_rmsnorm"
-    dt, dev, shape = x.dtype, x.device, x.shape
+    dt, shape, index = x.dtype, x.shape, x.get_device()
     if len(shape) != 2 or dt not in (torch.float32, torch.bfloat16):
         raise ValueError(f"{where}: x must be [rows, cols] of torch.float32 or torch.bfloat16")
     rows, cols = shape
-    address, stride = [], []
-    for t in (x, residual, sum_out, y):
-        if t is None:
-            address.append(None)
-            stride.append(0)
-            continue
-        step = t.stride()
-        if t.dtype != dt or t.shape != shape or step[1] != 1:
+    rs = ss = ys = 0
+    xs, step = x.stride()
+    for t in (residual, sum_out, y):
+        if t is not None and (t.dtype != dt or t.shape != shape or t.stride()[1] != step):
             raise ValueError(f"{where}: residual, sum_out and y must be like x, with unit column stride")
-        if t.device != dev:
+    if step != 1:
+        raise ValueError(f"{where}: x must have unit column stride")
+    if rows == 1:  # the stride of a single row is arbitrary
+        xs = rs = ss = ys = cols
+    else:
+        if residual is not None:
+            rs = residual.stride()[0]
+        if sum_out is not None:
+            ss = sum_out.stride()[0]
+        if y is not None:
+            ys = y.stride()[0]
+    if weight is not None and (weight.dtype != dt or weight.shape != (cols,) or not weight.is_contiguous()):
+        raise ValueError(f"{where}: weight must be contiguous [{cols}] of {dt}")
+    for t, width in ((codes, cols), (scale_bytes, cols // 128)):
+        if t is not None and (t.dtype != torch.uint8 or t.shape != (rows, width) or not t.is_contiguous()):
+            raise ValueError(f"{where}: codes and scale_bytes must be contiguous torch.uint8 [rows, cols] and [rows, cols / 128]")
+    for t in (x, weight, y, residual, sum_out, codes, scale_bytes):
+        if t is not None and (index < 0 or t.get_device() != index):
             raise ValueError(f"{where}: every tensor must be on the same CUDA device")
-        address.append(t.data_ptr())
-        stride.append(step[0] if rows > 1 else cols)  # the stride of a single row is arbitrary
-    for name, t, want, of in (("weight", weight, (cols,), dt), ("codes", codes, (rows, cols), torch.uint8),
-                              ("scale_bytes", scale_bytes, (rows, cols // 128), torch.uint8)):
-        if t is not None and (t.dtype != of or t.shape != want or not t.is_contiguous() or t.device != dev):
-            raise ValueError(f"{where}: {name} must be contiguous {list(want)} of {of} on x's device")
-    if dev.type != "cuda":
-        raise ValueError(f"{where}: every tensor must be on the same CUDA device")
-    _call_on(dev.index, _lib.moe_add_rmsnorm, where, address[0], stride[0], address[1], stride[1], _ptr(weight), eps, rows,
-             cols, MOE_F32 if dt == torch.float32 else MOE_BF16, address[2], stride[2], address[3], stride[3], _ptr(codes),
-             _ptr(scale_bytes), stream=stream)
+    _call_on(index, _lib.moe_add_rmsnorm, where,
+             (x.data_ptr(), xs, _ptr(residual), rs, _ptr(weight), eps, rows, cols,
+              MOE_F32 if dt == torch.float32 else MOE_BF16, _ptr(sum_out), ss, _ptr(y), ys, _ptr(codes), _ptr(scale_bytes)), stream)
 
 
 def moe_ep_recv_rows_bound(cfg, world, token_counts) -> int:
