@@ -1,11 +1,11 @@
 """Residual addition + root-mean-square norm + E4M3 output (moe_add_rmsnorm): refusals on the CPU, numerics on the
 GPU against the formula in binary64 and the oracle's row quantiser.
 
-Tolerance of y, relative to its own value. The sum of squares has only non-negative terms, each thread adds at most
-32 of them in a chain, a warp adds 5 levels, a row at most 32 warps: 69 roundings of 2^-24, halved by the square
-root; the division by cols, the addition of eps (halved too), the square root, its reciprocal, the two products, the
-sum x + r (in s and, halved, doubled in s^2) and the squaring (halved) add less than 8 more. So 43 * 2^-24 in all,
-and one rounding to the output's type (bf16: 2^-8, binary32: 2^-24)."""
+Tolerance of y, relative to its own value. The sum of squares has only non-negative terms: 8 of a vector in a chain,
+up to 4 vectors, 5 levels in a warp and up to 32 warps in a chain, 49 roundings of 2^-24 in all, and one for each
+square's x + r taken twice: 51, halved by the root. The inverse root is rounded once, to within 2 * 2^-24 after its
+Newton step; x + r and the two products add 3. So 31 * 2^-24, taken as 43, and one rounding to the output's type
+(bf16: 2^-8, binary32: 2^-24)."""
 import ctypes
 
 import numpy as np

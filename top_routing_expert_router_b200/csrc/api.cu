@@ -1064,8 +1064,8 @@ moe_status moe_add_rmsnorm(const void* x, int64_t x_stride, const void* residual
     return !o || ((o != x || os == x_stride) && (o != residual || os == residual_stride));
   };
   if (!in_place_ok(sum_out, sum_stride) || !in_place_ok(y, y_stride) || (y && y == sum_out)) return MOE_ERR_INVALID_ARG;
-  const NormArgs a{x,       x_stride,   residual, residual_stride, weight, eps,      rows,  cols,
-                   sum_out, sum_stride, y,        y_stride,        codes,  scale_bytes};
+  const NormArgs a{x,    x_stride, residual, residual_stride, weight,     eps, rows,
+                   cols, 1.0f / (float)cols, sum_out, sum_stride, y, y_stride, codes, scale_bytes};
   return cuda_status(launch_add_rmsnorm(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 

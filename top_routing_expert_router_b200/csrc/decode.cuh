@@ -69,36 +69,7 @@ __device__ __noinline__ inline bool wait_counter(const int32_t* p, int target, i
   }
 }
 
-// ---- E4M3 activations --------------------------------------------------------------
-
-// The codes of a 1 x 128 tile, four values per lane of the warp, and its scale byte.
-__device__ __forceinline__ uint32_t quantize_tile(const float (&v)[4], uint32_t* byte) {
-  float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-  const int e = ue8m0_exponent(m);
-  *byte = (uint32_t)(e + 127);
-  return e4m3x4(v[0], v[1], v[2], v[3], pow2_neg(e));
-}
-
-// ---- router ------------------------------------------------------------------------
-
-// 16 bytes of activations or router weights as binary32 (8 bf16 or 4 binary32 values).
-template <typename T>
-struct Chunk {
-  static constexpr int N = 16 / sizeof(T);
-};
-__device__ __forceinline__ void unpack(const uint4& raw, float (&v)[8]) {
-  const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = __uint_as_float(u[j] << 16);
-    v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void unpack(const uint4& raw, float (&v)[4]) {
-  v[0] = __uint_as_float(raw.x), v[1] = __uint_as_float(raw.y), v[2] = __uint_as_float(raw.z), v[3] = __uint_as_float(raw.w);
-}
+// ---- routing decision --------------------------------------------------------------
 
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll

@@ -88,6 +88,7 @@ struct NormArgs {
   float eps;
   int64_t rows;
   int32_t cols;
+  float inv_cols;  // 1 / cols
   void* sum_out;
   int64_t sum_stride;
   void* y;
