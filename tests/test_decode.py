@@ -43,6 +43,8 @@ def test_refusals():
     assert _call(bf, 65) == un                                                      # more tokens than the form takes
     assert _call(_cfg(cap_policy="drop", capacity_factor=1.0), 4) == un
     assert _call(_cfg(top_k=33, n_routed=64), 4, need=1 << 30) == un
+    assert _call(_cfg(moe_intermediate_size=1 << 27), 4, need=1 << 62) == un        # rows past 31 bits
+    assert _call(_cfg(moe_intermediate_size=1 << 24, n_shared=128), 4, need=1 << 62) == un
     assert _call(bf, -1) == bad
     assert _call(bf, 4, x=None) == bad and _call(bf, 4, x=264) == bad
     assert _call(bf, 4, y=None) == bad and _call(bf, 4, y=260) == bad

@@ -124,7 +124,8 @@ def _codes_of(y):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,cols", [(1, 8), (1, 7168), (3, 200), (5, 264), (7, 512), (61, 5120), (149, 1160), (200, 128),
-                                       (1000, 200), (2, 8192), (150, 8200), (3, 16392), (149, 32768), (2, 32768)])
+                                       (1000, 200), (2, 8192), (150, 8200), (3, 16392), (149, 32768), (2, 32768), (5000, 8),
+                                       (3001, 256), (2000, 1280), (1500, 4224), (700, 8192), (900, 16384)])
 @pytest.mark.parametrize("residual,weight", [(True, True), (False, False)])
 def test_matches_the_formula(dtype, rows, cols, residual, weight):
     x = _rand((rows, cols), dtype, 1)
@@ -146,8 +147,8 @@ def test_matches_the_formula(dtype, rows, cols, residual, weight):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_strided_rows_and_untouched_padding(dtype):
-    rows, cols = 37, 520
+@pytest.mark.parametrize("rows,cols", [(37, 520), (1000, 104), (1000, 5000), (300, 1032)])
+def test_strided_rows_and_untouched_padding(dtype, rows, cols):
     x, r = _rand((rows, cols), dtype, 4), _rand((rows, cols), dtype, 5)
     w = _rand((cols,), dtype, 6)
     (_, xv), (_, rv) = _strided(x, 24), _strided(r, 8)
@@ -158,7 +159,7 @@ def test_strided_rows_and_untouched_padding(dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows,cols", [(3, 7168), (500, 1024)])
+@pytest.mark.parametrize("rows,cols", [(3, 7168), (500, 1024), (1501, 256), (700, 7168), (400, 16384)])
 def test_in_place(rows, cols):
     x, r = _rand((rows, cols), torch.bfloat16, 7), _rand((rows, cols), torch.bfloat16, 8)
     w = _rand((cols,), torch.bfloat16, 9)

@@ -960,6 +960,12 @@ moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, con
   Ctx c;
   MOE_TRY(begin(cfg, n, ws, ws_bytes, stream, &c));
   if (cfg->cap_policy != MOE_CAP_NONE || n > MOE_DECODE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  {  // weight rows and tiles are counted in 32 bits
+    const int64_t widest = cfg->moe_intermediate_size > cfg->d_model ? cfg->moe_intermediate_size : cfg->d_model;
+    const int64_t most = ((int64_t)1 << 31) - 256;
+    if (cfg->n_routed * widest >= most || (int64_t)cfg->n_shared * cfg->moe_intermediate_size >= most)
+      return MOE_ERR_UNSUPPORTED;
+  }
   if (!tok_ok(x, n) || !tok_ok(y, n) || !weights || !ptr_ok(weights->w_router)) return MOE_ERR_INVALID_ARG;
   if ((topk_idx_opt && !tok_ok(topk_idx_opt, n)) || (topk_w_opt && !tok_ok(topk_w_opt, n)) ||
       (counts_opt && !aligned(counts_opt, 4)) || (diag_opt && !aligned(diag_opt, 16)))
@@ -1024,7 +1030,7 @@ moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, con
   a.ctr = c.at<int32_t>(c.p.dctr);
   a.status = c.status();
   const bool tensor = f.dtype != MOE_F32;
-  if (tensor && !decode_tc_supported(a)) return MOE_ERR_UNSUPPORTED;
+  if (tensor && !decode_tc_supported()) return MOE_ERR_UNSUPPORTED;
   a.clear = c.ws;
   a.clear_bytes = (int32_t)align_up((int64_t)c.p.dctr + decode_counters(a.cut, a.d, a.E, a.I, a.Is) * 4, 16);
   MOE_CUDA(launch_decode_router(a, c.s));

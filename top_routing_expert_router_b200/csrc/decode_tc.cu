@@ -776,10 +776,7 @@ int64_t decode_counters(const DecodeSplits& cut, int32_t d, int32_t E, int32_t I
   return kCtrExpert + E + 1 + ceil_div(d, kMinColumns) + (cut.s1 > 1 || cut.s1s > 1 ? E * ceil_div(I, kRows) + ceil_div(Is, kRows) : 0);
 }
 
-bool decode_tc_supported(const DecodeArgs& a) {
-  const int64_t widest = a.I > a.d ? a.I : a.d;
-  return encode_fn() != nullptr && a.E * widest < ((int64_t)1 << 31) - 256;  // TMA row coordinates
-}
+bool decode_tc_supported() { return encode_fn() != nullptr; }
 
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s) {
   const bool fp8 = a.dtype == MOE_FP8;

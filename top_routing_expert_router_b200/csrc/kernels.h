@@ -216,7 +216,7 @@ int64_t decode_counters(const DecodeSplits& cut, int32_t d, int32_t E, int32_t I
 cudaError_t launch_decode_router(const DecodeArgs& a, cudaStream_t s);  // first: logits, x's codes, cleared counters
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t s);    // then the layer: binary32,
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s);      // or bf16 and FP8 experts
-bool decode_tc_supported(const DecodeArgs& a);
+bool decode_tc_supported();  // whether the driver has tensor maps
 
 // Capacity rule over the ranking on many SMs (capacity.cu): a cooperative grid, one token per
 // thread, one round per fill event. Needs capacity_grid_scratch_bytes of scratch (16-byte aligned)
