@@ -229,17 +229,20 @@ moe_status moe_layer_forward(const moe_config* cfg, int64_t n, const void* x, co
                              moe_diag* diag_opt, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
- * Whole layer for the few tokens of a decode step, in one kernel launch:
+ * Whole layer for the few tokens of a decode step, in two kernel launches (the
+ * router's logits; everything else, set up while the first runs):
  * n <= MOE_DECODE_MAX_TOKENS, otherwise MOE_ERR_UNSUPPORTED. Arguments and
  * outputs are those of moe_layer_forward, every dtype and scoring; a capacity
  * is a property of a large batch and cfg->cap_policy must be MOE_CAP_NONE
- * (MOE_ERR_UNSUPPORTED otherwise).
+ * (MOE_ERR_UNSUPPORTED otherwise, as for E * max(d, I) or n_shared * I of about
+ * 2^31 and more).
  *   x_codes_opt [n, d], x_scale_bytes_opt [n, d / 128]: MOE_FP8 only, both or
  *   neither: the E4M3 tiles of x when the caller has them (moe_add_rmsnorm,
  *   moe_quantize_fp8); NULL: the call quantises x. The router always reads x.
  * Arithmetic: router logits are binary64 sums of exact products, so the
  * indices are those of the binary64 definition with no second pass (diag's
- * refined_* stay 0); expert products accumulate in binary32; the intermediate
+ * overflowed, dropped and refined_* are 0); a token whose x is not finite has
+ * NaN logits and takes the lowest experts; expert products accumulate in binary32; the intermediate
  * is rounded to the activation type (then to E4M3 for MOE_FP8) as in
  * moe_expert_ffn; expert outputs stay binary32 and are rounded once, as y.
  * The results differ from moe_layer_forward's by those roundings.

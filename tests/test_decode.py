@@ -1,4 +1,4 @@
-"""The one-launch layer for few tokens (moe_layer_decode): refusals on the CPU; on the GPU every dtype and scoring
+"""The two-launch layer for few tokens (moe_layer_decode): refusals on the CPU; on the GPU every dtype and scoring
 against the fp64 oracle, and the calls the documentation allows.
 
 Tolerances of y are the layer parity tests' (2e-2 for bf16 and FP8, 1e-4 for binary32, relative to the larger of the

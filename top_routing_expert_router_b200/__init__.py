@@ -207,7 +207,7 @@ def moe_layer_forward(cfg, n, x, weights, y, ws, topk_idx=None, topk_w=None, cou
 
 def moe_layer_decode(cfg, n, x, weights, y, ws, topk_idx=None, topk_w=None, counts=None, diag=None, x_codes=None,
                      x_scale_bytes=None, stream=None):
-    """moe_layer_forward for n <= MOE_DECODE_MAX_TOKENS tokens in one launch; x_codes and x_scale_bytes are x's E4M3
+    """moe_layer_forward for n <= MOE_DECODE_MAX_TOKENS tokens in two launches; x_codes and x_scale_bytes are x's E4M3
     tiles (MOE_FP8) when the caller has them. Every tensor is contiguous and on ws's device."""
     where = "moe_layer_decode"
     index, d, slots = ws.get_device(), cfg.d_model, 4 * n * cfg.top_k

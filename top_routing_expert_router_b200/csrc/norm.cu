@@ -82,15 +82,15 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
-// y = s * scale * inv (* w): scale is 1, or 2^-80 for a row whose squares overflow.
+// y = s * scale * (inv + inv_lo) (* w): scale is 1, or 2^-80 for a row whose squares overflow.
 struct Norm {
-  float scale, inv;
+  float scale, inv, inv_lo;
 };
 
-// 1 / sqrt(ss / cols + eps), rounded once: an approximation and one Newton step whose residual
-// 1 - a inv^2 is formed by fused multiply-adds. Fewer values fall on the other side of a bf16 or E4M3
-// tie than with a square root and two divisions, and it is quicker. (The two products of a value
-// compensated as well took 7 to 20 % longer.)
+// 1 / sqrt(ss / cols + eps) to about twice binary32's precision: an approximation and one Newton
+// step whose residual 1 - a inv^2 is formed by fused multiply-adds. With the product of a value
+// compensated too (finish_vector), the value is rounded once, from an error near 2^-26: a bf16 or
+// E4M3 code that differs from the exact norm's is four times as rare as with three rounded products.
 __device__ __forceinline__ Norm inverse_rms(float ss, const NormArgs& n, float eps, float scale) {
   const float q = ss * n.inv_cols, q_lo = fmaf(-q, (float)n.cols, ss) * n.inv_cols;
   const float a = q + eps, z = a - q;
@@ -98,7 +98,7 @@ __device__ __forceinline__ Norm inverse_rms(float ss, const NormArgs& n, float e
   const float inv = rsqrtf(a), p = inv * inv;
   const float r = fmaf(-a, p, 1.0f) - a * fmaf(inv, inv, -p) - a_lo * p;
   // (r means nothing where a is infinite, or so small that p overflows)
-  return Norm{scale, a >= 0x1p-120f && a < INFINITY ? fmaf(0.5f * inv, r, inv) : inv};
+  return Norm{scale, inv, a >= 0x1p-120f && a < INFINITY ? 0.5f * inv * r : 0.0f};
 }
 
 // The row's Norm. square_sum(scale, store) sums (s * scale)^2 over the row (and stores sum_out).
@@ -123,21 +123,45 @@ __device__ __forceinline__ Norm norm_of(const NormArgs& a, bool live, int local,
   return n;
 }
 
+// v rounded to T: stored at p where there is one, and back in v.
+__device__ __forceinline__ void round_store8(float* p, float (&v)[kVec]) {
+  if (p) store8(p, v);
+}
+__device__ __forceinline__ void round_store8(bf16* p, float (&v)[kVec]) {
+  Raw<bf16> r;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&r.a);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+  if (p) *reinterpret_cast<uint4*>(p) = r.a;
+  values(r, v);
+}
+
 // Vector `at` of a row from its s in y (not `on`: past the row): y and its codes, as asked for.
 template <typename T>
 __device__ __forceinline__ void finish_vector(const NormArgs& a, int64_t row, int at, bool on, const Norm& n,
                                               const Raw<T>& rw, float (&y)[kVec]) {
   if (on) {
+    if (n.scale != 1.0f) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) y[j] *= n.scale;
+    }
+    float lo[kVec];  // what the product's rounding and inv leave out
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const float t = y[j] * n.inv;
+      lo[j] = fmaf(y[j], n.inv_lo, fmaf(y[j], n.inv, -t));
+      y[j] = t;
+    }
     if (a.w) {
       float q[kVec];
       values(rw, q);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) y[j] = to_f32(from_f32<T>(y[j] * n.scale * n.inv * q[j]));
+      for (int j = 0; j < kVec; ++j) y[j] = fmaf(y[j], q[j], lo[j] * q[j]);
     } else {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) y[j] = to_f32(from_f32<T>(y[j] * n.scale * n.inv));
+      for (int j = 0; j < kVec; ++j) y[j] += lo[j];
     }
-    if (a.y) store8(static_cast<T*>(a.y) + row * a.y_stride + at * kVec, y);
+    round_store8(a.y ? static_cast<T*>(a.y) + row * a.y_stride + at * kVec : nullptr, y);
   }
   if (!a.codes) return;
   float m = 0.0f;  // with codes, `on` is uniform over each 16 lanes (cols % 128 == 0)
