@@ -9,7 +9,7 @@
 // tiles (shared experts first), down tiles. A unit waits only for units that were claimed before
 // it, so some block is running each of them and every wait ends, whatever share of the grid is
 // resident: no cooperative launch, and calls on several streams may overlap on the GPU. Waits are
-// bounded all the same (kDecodeTimeoutNs).
+// bounded all the same (kDecodeTimeoutCycles).
 //
 // Sums are deterministic: no floating-point atomics; whichever block adds the expert rows of a
 // column range takes them in slot order.
@@ -24,7 +24,9 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr uint64_t kDecodeTimeoutNs = 2000000000ull;  // 2 s for any single wait
+// Limit of any single wait: 2 s at the highest clock. (Reading the SM's clock takes a few cycles, where
+// %globaltimer takes long enough to delay a wait that ends meanwhile.)
+constexpr long long kDecodeTimeoutCycles = 4000000000ll;
 
 // Counter words (zeroed before the launch).
 enum {
@@ -55,12 +57,12 @@ __device__ __forceinline__ int add_release(int32_t* p, int v) {
 // One thread waits until *p >= target. False once the call is abandoned.
 __device__ __noinline__ inline bool wait_counter(const int32_t* p, int target, int32_t* ctr, moe_diag* status) {
   if (ld_acquire(p) >= target) return true;
-  const uint64_t t0 = ptx::globaltimer();
+  const long long t0 = clock64();
   for (uint32_t it = 1;; ++it) {
     if (ld_acquire(p) >= target) return true;
     if ((it & 63u) == 0) {
       if (ld_acquire(ctr + kCtrAbort)) return false;
-      if (ptx::globaltimer() - t0 > kDecodeTimeoutNs) {
+      if (clock64() - t0 > kDecodeTimeoutCycles) {
         atomicExch(ctr + kCtrAbort, 1);
         set_status(status, MOE_ERR_TIMEOUT);
         return false;

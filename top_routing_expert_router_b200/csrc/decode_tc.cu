@@ -46,13 +46,14 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSfCol0 = 256;           // after two pairs of accumulators of at most 64 columns
 constexpr uint32_t kSfCols = 12;            // per slot: D0's rows, D1's rows, the tokens
 constexpr size_t kSmemLimit = 232448;
-// Tiles are cut along k until there are about this many, in parts of at least kMinPart k blocks. Few
-// experts (a token or two) leave fewer tiles than SMs, and one SM draws at most about 65 GB/s. The
-// routed gate/up tiles: a part costs a round trip through L2 (DeepSeek-V3 shapes, one token, 128
-// tiles: FP8 99 us whole, 97 in two parts; 8 experts of 16 tiles, top-1: 81 us whole, 44 in ten). The
-// shared ones get a part for every SM, as they stream while the router runs. Down tiles join their
-// parts in the combine (Mixtral shapes, one token, 32 tiles of 7.3 MB: 201 us whole, 135 in ten parts).
-constexpr int kTiles1 = 148, kTiles2 = 296, kMinPart = 8, kMaxParts = 16;
+// Few experts (a token or two) leave fewer tiles than SMs, and one SM draws at most about 65 GB/s, so
+// tiles are cut along k: into as many parts as keep the parts within one turn of the SMs (two turns for
+// down tiles), of at least kMinPart k blocks; tiles of nearly one (two) turns are halved. A part of a
+// gate/up tile costs a round trip through L2; down tiles join their parts in the combine. Measured at one
+// token: 16 gate/up tiles 81 us whole, 40.5 in nine parts; 96 tiles 66.8 us whole, 76.4 halved; 128 tiles
+// and 252 down tiles (DeepSeek-V3 shapes, FP8) 79 us with both halved, 83 with either whole; 32 down tiles
+// of 7.3 MB (Mixtral shapes) 201 us whole, 130 in nine parts.
+constexpr int kSms = 148, kMinPart = 8, kMaxParts = 16;
 
 struct __align__(16) Ctl {
   uint64_t full[kMaxStages];   // weights' and tokens' arrivals
@@ -92,12 +93,12 @@ struct TcShape {
 __device__ __noinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* ctr, moe_diag* st) {
   const uint32_t b = smem_u32(bar);
   if (mbar_try(b, parity)) return true;
-  const uint64_t t0 = globaltimer();
+  const long long t0 = clock64();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try(b, parity)) return true;
     if ((it & 255u) == 0) {
       if (*reinterpret_cast<volatile int32_t*>(&ctl->abort)) return false;
-      if (globaltimer() - t0 > kDecodeTimeoutNs) {
+      if (clock64() - t0 > kDecodeTimeoutCycles) {
         atomicExch(&ctl->abort, 1);
         atomicExch(ctr + kCtrAbort, 1);
         set_status(st, MOE_ERR_TIMEOUT);
@@ -247,6 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  if (warp == 3 && lane < 9)  // the first copies do not wait for their descriptors
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.gate + lane)) : "memory");
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem_base)),
                  "r"(kTmemCols)
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                   g[j] = u[j] = 0.0f;
                   if (!((mine >> j) & 1u) || c >= tl.Ie) continue;
                   const float* o = part + (int64_t)from++ * tl.parts * 2 * tl.Ie + c;
-  #pragma unroll 4
+  #pragma unroll 8
                   for (int p = 0; p < tl.parts; ++p) {
                     g[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie);
                     u[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie + tl.Ie);
@@ -746,14 +749,13 @@ cudaError_t launch_t(const DecodeArgs& a, const DecodeMaps& maps, const TcShape&
   return launch_early(decode_tc_kernel<FP8>, grid, kThreads, smem, s, maps, a, sh);
 }
 
-// Parts of a k axis of nkb blocks, so that `tiles` tiles of it make about `target`, each of at least
-// kMinPart blocks (FP8: whole words of four scale bytes).
-void split_k(int64_t tiles, int64_t target, int64_t nkb, int32_t* parts, int32_t* per) {
-  int64_t p = ceil_div(target, tiles > 0 ? tiles : 1);
+// A k axis of nkb blocks in about `p` parts, each of at least kMinPart blocks (FP8: of whole scale
+// words, four blocks).
+void split_k(int64_t p, int64_t nkb, bool fp8, int32_t* parts, int32_t* per) {
   if (p > nkb / kMinPart) p = nkb / kMinPart;
   if (p > kMaxParts) p = kMaxParts;
   if (p < 1) p = 1;
-  *per = (int32_t)align_up(nkb > 0 ? ceil_div(nkb, p) : 1, 4);
+  *per = (int32_t)align_up(nkb > 0 ? ceil_div(nkb, p) : 1, fp8 ? 4 : 1);
   *parts = nkb > 0 ? (int32_t)ceil_div(nkb, *per) : 1;
 }
 
@@ -764,11 +766,14 @@ DecodeSplits decode_splits(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I
   if (dtype == MOE_F32) return c;
   const int64_t ke = dtype == MOE_FP8 ? 128 : 64;
   const int64_t active = n * k < E ? n * k : E;  // experts at most
-  const int64_t tiles2 = ceil_div(d, kColumns);
-  split_k(active * ceil_div(I, kRows), kTiles1, ceil_div(d, ke), &c.s1, &c.per1);
-  split_k(ceil_div(Is, kRows), kTiles1, ceil_div(d, ke), &c.s1s, &c.per1s);
-  split_k((active + (Is > 0)) * tiles2, kTiles2, ceil_div(I, ke), &c.s2, &c.per2);
-  split_k((active + (Is > 0)) * tiles2, kTiles2, ceil_div(Is, ke), &c.s2s, &c.per2s);
+  const int64_t tiles1 = active * ceil_div(I, kRows), tiles1s = ceil_div(Is, kRows);
+  const int64_t tiles2 = (active + (Is > 0)) * ceil_div(d, kColumns);
+  const bool fp8 = dtype == MOE_FP8;
+  split_k(tiles1 >= kSms * 3 / 4 && tiles1 < kSms ? 2 : kSms / tiles1, ceil_div(d, ke), fp8, &c.s1, &c.per1);
+  split_k(tiles1s > 0 ? kSms / tiles1s : 1, ceil_div(d, ke), fp8, &c.s1s, &c.per1s);
+  const int64_t parts2 = tiles2 >= kSms && tiles2 < 2 * kSms ? 2 : 2 * kSms / tiles2;
+  split_k(parts2, ceil_div(I, ke), fp8, &c.s2, &c.per2);
+  split_k(parts2, ceil_div(Is, ke), fp8, &c.s2s, &c.per2s);
   return c;
 }
 
