@@ -100,9 +100,9 @@ struct __align__(16) DecideScratch {
   int idx[kMaxTopK];
 };
 
-// The block's largest value (SUM: sum) of v over 256 threads, in a fixed order.
+// The block's largest value (SUM: sum) of v over the first `warps` warps, in a fixed order.
 template <bool SUM, typename Sync>
-__device__ __noinline__ double block_reduce(double v, double* part, int tid, Sync sync) {
+__device__ __noinline__ double block_reduce(double v, double* part, int tid, int warps, Sync sync) {
 #pragma unroll
   for (int off = 16; off; off >>= 1) {
     const double o = __shfl_xor_sync(kFull, v, off);
@@ -111,8 +111,7 @@ __device__ __noinline__ double block_reduce(double v, double* part, int tid, Syn
   if ((tid & 31) == 0) part[tid >> 5] = v;
   sync();
   v = part[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) v = SUM ? v + part[i] : fmax(v, part[i]);
+  for (int i = 1; i < warps; ++i) v = SUM ? v + part[i] : fmax(v, part[i]);
   sync();
   return v;
 }
@@ -178,9 +177,11 @@ __device__ void decide_token(const DecodeArgs& a, int t, float bias, DecideScrat
   }
   sc->hi[e] = (uint32_t)(key >> 32);
   if (a.score_fn == MOE_SCORE_SOFTMAX) {
-    const double m = block_reduce<false>(live ? l : -INFINITY, sc->part, tid, sync);
+    const int warps = (a.E + 31) / 32;
+    const double m = block_reduce<false>(live ? l : -INFINITY, sc->part, tid, warps, sync);
     score = live ? exp(l - m) : 0.0;
-    score /= block_reduce<true>(score, sc->part, tid, sync);
+    // (over the kept slots the sum of all experts cancels)
+    if (!a.renorm) score /= block_reduce<true>(score, sc->part, tid, warps, sync);
   }
   const int per_warp = min(a.k, 32);
   if (w0 < a.E) {
