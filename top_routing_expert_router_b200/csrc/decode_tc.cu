@@ -48,12 +48,12 @@ constexpr uint32_t kSfCols = 12;            // per slot: D0's rows, D1's rows, t
 constexpr size_t kSmemLimit = 232448;
 // Few experts (a token or two) leave fewer tiles than SMs, and one SM draws at most about 65 GB/s, so
 // tiles are cut along k: into as many parts as keep the parts within one turn of the SMs (two turns for
-// down tiles), of at least kMinPart k blocks; tiles of nearly one (two) turns are halved. A part of a
+// down tiles), of at least what the ring holds, kMinPart k blocks; tiles of nearly one (two) turns are halved. A part of a
 // gate/up tile costs a round trip through L2; down tiles join their parts in the combine. Measured at one
 // token: 16 gate/up tiles 81 us whole, 40.5 in nine parts; 96 tiles 66.8 us whole, 76.4 halved; 128 tiles
 // and 252 down tiles (DeepSeek-V3 shapes, FP8) 79 us with both halved, 83 with either whole; 32 down tiles
 // of 7.3 MB (Mixtral shapes) 201 us whole, 130 in nine parts.
-constexpr int kSms = 148, kMinPart = 8, kMaxParts = 16;
+constexpr int kSms = 148, kMinPart = 6, kMaxParts = 16;
 
 struct __align__(16) Ctl {
   uint64_t full[kMaxStages];   // weights' and tokens' arrivals
