@@ -89,8 +89,10 @@ struct Norm {
 
 // 1 / sqrt(ss / cols + eps) to about twice binary32's precision: an approximation and one Newton
 // step whose residual 1 - a inv^2 is formed by fused multiply-adds. With the product of a value
-// compensated too (finish_vector), the value is rounded once, from an error near 2^-26: a bf16 or
-// E4M3 code that differs from the exact norm's is four times as rare as with three rounded products.
+// compensated too (finish_vector), the value is rounded once. Of 4096 x 5120 binary32 values 34 %
+// differ from the exact norm rounded once, against 51 % with three rounded products; of 29 million
+// bf16 values 223 do, nearly all by the rounding of s = x + r to binary32 where x and r are far apart.
+// (The sum of squares with its remainder carried along would leave 202, and takes 4 to 18 % longer.)
 __device__ __forceinline__ Norm inverse_rms(float ss, const NormArgs& n, float eps, float scale) {
   const float q = ss * n.inv_cols, q_lo = fmaf(-q, (float)n.cols, ss) * n.inv_cols;
   const float a = q + eps, z = a - q;
