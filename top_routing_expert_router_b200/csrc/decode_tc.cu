@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     if (lane == 0) {
       int stage = 0, q = 0, i = 0;
       uint32_t phase = 0, qphase = 0;
+      [[maybe_unused]] uint32_t sf_slot = 0;  // FP8: scale words of four k blocks, two slots in turn
       bool ok = true, issued = false;
       for (;; ++i) {
         if (!(ok = wait(&ctl->tile_full[q], qphase))) break;
@@ -366,7 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
           const uint32_t sa = smem_u32(smem + stage * sh.stage_bytes);
           const uint64_t a0 = sw128_desc(sa), a1 = sw128_desc(sa + kABytes), b = sw128_desc(sa + 2 * kABytes);
           if constexpr (FP8) {
-            const uint32_t sf = tmem_base + kSfCol0 + kSfCols * (uint32_t)((kb >> 2) & 1);
+            if ((kb & 3) == 0) sf_slot ^= 1u;
+            const uint32_t sf = tmem_base + kSfCol0 + kSfCols * sf_slot;
             if ((kb & 3) == 0) {
               const uint32_t ss = smem_u32(smem + sh.sf_off + stage * 3 * kSfBytes);
               sf_copy(sf, sf_desc(ss));
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 if (!mine) continue;
                 float g[4], u[4];
                 tmem_ld4x2(d0 + (uint32_t)t0, d1 + (uint32_t)t0, g, u);
-  #pragma unroll
+#pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   if (!((mine >> j) & 1u)) continue;
                   float* o = part + ((int64_t)row++ * tl.parts + tl.part) * 2 * tl.Ie + c;
@@ -597,12 +599,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
               float g[4], u[4];
               if (tl.parts > 1) {
                 int from = row;
-  #pragma unroll
+#pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   g[j] = u[j] = 0.0f;
                   if (!((mine >> j) & 1u) || c >= tl.Ie) continue;
                   const float* o = part + (int64_t)from++ * tl.parts * 2 * tl.Ie + c;
-  #pragma unroll 8
+#pragma unroll 8
                   for (int p = 0; p < tl.parts; ++p) {
                     g[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie);
                     u[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie + tl.Ie);
@@ -611,10 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
               } else {
                 tmem_ld4x2(d0 + (uint32_t)t0, d1 + (uint32_t)t0, g, u);
               }
-  #pragma unroll
+#pragma unroll
               for (int j = 0; j < 4; ++j) g[j] = silu(g[j]) * u[j];
               if constexpr (FP8) {
-  #pragma unroll
+#pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   if (!((mine >> j) & 1u)) continue;
                   g[j] = to_f32(from_f32<bf16>(g[j]));
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 named_sync<2, 128>();
                 uint8_t* hq = static_cast<uint8_t*>(s ? a.hs : a.h);
                 uint8_t* hb = s ? a.hs_scale : a.h_scale;
-  #pragma unroll
+#pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   if (!((mine >> j) & 1u)) continue;
                   const float4 m4 = ctl->amax[j];
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 named_sync<2, 128>();  // amax is the next columns'
               } else {
                 bf16* h = static_cast<bf16*>(s ? a.hs : a.h);
-  #pragma unroll
+#pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   if (!((mine >> j) & 1u)) continue;
                   if (c < tl.Ie) h[(int64_t)row * tl.Ie + c] = from_f32<bf16>(g[j]);
@@ -656,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             for (int t0 = 0; t0 < tl.m; t0 += 4) {
               float v0[4], v1[4];
               tmem_ld4x2(d0 + (uint32_t)t0, (two ? d1 : d0) + (uint32_t)t0, v0, v1);
-  #pragma unroll
+#pragma unroll
               for (int j = 0; j < 4; ++j) {
                 if (t0 + j >= tl.m) break;
                 float* o = out + (int64_t)(t0 + j) * a.d + tl.r0 + r;
@@ -717,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     }
   }
 
+  __syncwarp();  // lanes that had no part in their warp's work
   fence_before();
   __syncthreads();
   fence_after();
