@@ -242,13 +242,15 @@ moe_status moe_layer_forward(const moe_config* cfg, int64_t n, const void* x, co
  * Arithmetic: router logits are binary64 sums of exact products, so the
  * indices are those of the binary64 definition with no second pass (diag's
  * overflowed, dropped and refined_* are 0); a token whose x is not finite has
- * NaN logits and takes the lowest experts; expert products accumulate in binary32; the intermediate
- * is rounded to the activation type (then to E4M3 for MOE_FP8) as in
- * moe_expert_ffn; expert outputs stay binary32 and are rounded once, as y.
- * The results differ from moe_layer_forward's by those roundings.
- * ws: moe_workspace_size() bytes; two calls that overlap on the GPU need two
- * workspaces (graphs replayed at once too). Waits between the launch's own
- * blocks are bounded (2 s, then MOE_ERR_TIMEOUT in the status word).
+ * NaN logits and takes the lowest experts; expert products accumulate in
+ * binary32; the intermediate is rounded to the activation type (then to E4M3
+ * for MOE_FP8) as in moe_expert_ffn; expert outputs stay binary32 and are
+ * rounded once, as y. The results differ from moe_layer_forward's by those
+ * roundings.
+ * ws: moe_workspace_size() bytes of this n or of any larger one; two calls that
+ * overlap on the GPU need two workspaces (graphs replayed at once too). Waits
+ * between the launch's own blocks are bounded (2 s, then MOE_ERR_TIMEOUT in the
+ * status word).
  */
 #define MOE_DECODE_MAX_TOKENS 64
 moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, const uint8_t* x_codes_opt,

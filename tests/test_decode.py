@@ -63,6 +63,30 @@ def test_refusals():
     assert _call(bf, 4, w=no, need=0) == moe.MOE_ERR_WORKSPACE and _call(f8, 4, w=no) == bad
 
 
+@pytest.mark.parametrize("name", ["tiny_f32", "mixtral_small", "mixtral_8x7b", "deepseek_v3_small", "deepseek_v3_prefill",
+                                  "deepseek_v3_decode_small_fp8", "deepseek_v3_decode_fp8_32e", "ragged_small"])
+def test_one_workspace_serves_fewer_tokens_too(name):
+    """A workspace is sized for the largest batch; every call of up to 64 tokens takes it."""
+    cfg = H.cfg_for(W.get(name))
+    size = [moe.moe_workspace_size(cfg, n) for n in [*range(1, 81), 100, 127, 128, 129, 200, 257, 500]]
+    assert size[:64] == sorted(size[:64]) and min(size[64:]) >= size[63]
+    for n in (1, 2, 7, 33, 64):  # (the refusal is of x, a null pointer)
+        assert _call(cfg, n, x=None, need=size[79]) == moe.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (8, 2), (40, 32), (250, 5), (256, 8), (256, 1)])
+def test_workspace_grows_with_the_tokens_for_every_shape(E, k):
+    for d in (8, 136, 1032, 4096, 7168):
+        for I in (8, 128, 1000, 2048, 14336):
+            for shared in (0, 1, 3):
+                for dtype in ("f32", "bf16", "fp8"):
+                    if dtype == "fp8" and (d % 128 or I % 128 or I > 8192):
+                        continue
+                    cfg = moe.make_config(d_model=d, n_routed=E, top_k=k, moe_intermediate_size=I, n_shared=shared, dtype=dtype)
+                    size = [moe.moe_workspace_size(cfg, n) for n in range(1, 67)]
+                    assert size == sorted(size), (d, I, shared, dtype)
+
+
 def test_binding_refuses_what_it_cannot_hand_over():
     cfg = _cfg()
     t = torch.zeros(4, 512, dtype=torch.bfloat16)
@@ -183,6 +207,14 @@ def test_optional_outputs_left_out():
     a, b = Call(w, dev)(), Call(w, dev)
     moe.moe_layer_decode(b.cfg, w.n, dev["x"], b.weights, b.y, b.ws)
     assert torch.equal(a.y, b.y)
+
+
+@pytest.mark.gpu
+def test_workspace_of_a_larger_batch():
+    w, host, dev = _get("deepseek_v3_small", 5)
+    c = Call(w, dev)
+    c.ws = torch.full((moe.moe_workspace_size(c.cfg, 200),), 0xFF, dtype=torch.uint8, device="cuda")
+    c().check(_oracle(w, host))
 
 
 @pytest.mark.gpu

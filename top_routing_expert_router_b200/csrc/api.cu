@@ -100,11 +100,6 @@ Plan make_plan(const moe_config& c, int64_t n, int32_t ep_world = 0, int64_t ep_
     return at;
   };
   p.diag = take(sizeof(moe_diag));
-  // the counters right behind the status word: one memset clears both
-  const bool few = !ep && n > 0 && n <= MOE_DECODE_MAX_TOKENS && c.cap_policy == MOE_CAP_NONE;
-  const DecodeSplits cut = few ? decode_splits(n, c.d_model, c.n_routed, c.top_k, c.moe_intermediate_size, (int32_t)Is, c.dtype)
-                               : DecodeSplits{};
-  p.dctr = take(few ? (size_t)decode_counters(cut, c.d_model, c.n_routed, c.moe_intermediate_size, (int32_t)Is) * 4 : 0);
   p.logits = take((size_t)router_splits(c, n) * n * logits_ld(c) * 4);
   // the queue of tokens left to the binary64 router (one-pass router, or the first pass of the
   // two-kernel router), and their candidate experts: four counters, the candidate table, its
@@ -149,13 +144,20 @@ Plan make_plan(const moe_config& c, int64_t n, int32_t ep_world = 0, int64_t ep_
   p.sfb = take(fp8 ? sfb_bytes(fg, I, d) : 0);
   p.sfbs = take(fp8 && Is > 0 ? sfb_bytes(1, Is, d) : 0);
   p.ep_off = take(ep ? (size_t)(fg + 1) * 4 : 0);
-  p.dlog = take(few ? (size_t)n * c.n_routed * 8 : 0);
-  p.dgu = take(few && (cut.s1 > 1 || cut.s1s > 1) ? (size_t)2 * (cut.s1 * nk * I + cut.s1s * n * Is) * 4 : 0);
-  p.deo = take(few ? (size_t)cut.s2 * nk * d * 4 : 0);
-  p.des = take(few && Is > 0 ? (size_t)cut.s2s * n * d * 4 : 0);
-  p.dxs = take(few && fp8 ? (size_t)n * (d / 128) : 0);
-  p.dhs = take(few && fp8 ? (size_t)nk * (I / 128) : 0);
-  p.dhss = take(few && fp8 && Is > 0 ? (size_t)n * (Is / 128) : 0);
+  // for moe_layer_decode of at most n tokens, whose needs grow with its tokens (decode_rows)
+  const int64_t few = ep || c.cap_policy != MOE_CAP_NONE ? 0 : n < MOE_DECODE_MAX_TOKENS ? n : MOE_DECODE_MAX_TOKENS;
+  if (few > 0) {
+    const DecodeSplits cut = decode_splits(few, c.d_model, c.n_routed, c.top_k, c.moe_intermediate_size, (int32_t)Is, c.dtype);
+    const DecodeRows rows = decode_rows(cut, few, c.d_model, c.top_k, c.moe_intermediate_size, (int32_t)Is, c.dtype);
+    p.dctr = take((size_t)decode_counters(c.d_model, c.n_routed, c.moe_intermediate_size, (int32_t)Is) * 4);
+    p.dlog = take((size_t)few * c.n_routed * 8);
+    p.dgu = take((size_t)2 * (rows.gu * I + rows.gus * Is) * 4);
+    p.deo = take((size_t)rows.eo * d * 4);
+    p.des = take((size_t)rows.es * d * 4);
+    p.dxs = take(fp8 ? (size_t)few * (d / 128) : 0);
+    p.dhs = take(fp8 ? (size_t)few * c.top_k * (I / 128) : 0);
+    p.dhss = take(fp8 ? (size_t)few * (Is / 128) : 0);
+  }
   p.total = off;
   return p;
 }
@@ -1031,8 +1033,7 @@ moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, con
   a.status = c.status();
   const bool tensor = f.dtype != MOE_F32;
   if (tensor && !decode_tc_supported()) return MOE_ERR_UNSUPPORTED;
-  a.clear = c.ws;
-  a.clear_bytes = (int32_t)align_up((int64_t)c.p.dctr + decode_counters(a.cut, a.d, a.E, a.I, a.Is) * 4, 16);
+  a.ctr_bytes = (int32_t)align_up(decode_counters(a.d, a.E, a.I, a.Is) * 4, 16);
   MOE_CUDA(launch_decode_router(a, c.s));
   return cuda_status(tensor ? launch_decode_tc(a, c.s) : launch_decode_simt(a, c.s));
 }

@@ -156,8 +156,10 @@ __global__ void __launch_bounds__(32 * kWarps) decode_router_kernel(DecodeArgs a
   __shared__ double part[kWarps * 2 * kRouterTokens];
   wait_for_earlier_kernels();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the layer's kernel sets itself up meanwhile
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.clear_bytes / 16; i += 32 * kWarps) static_cast<uint4*>(a.clear)[i] = make_uint4(0, 0, 0, 0);
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < a.ctr_bytes / 16; i += 32 * kWarps) reinterpret_cast<uint4*>(a.ctr)[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) a.status->status = MOE_OK;
+  }
   const int u = blockIdx.x;
   if (u < quants) {
     const int i = u * kWarps + (threadIdx.x >> 5);

@@ -70,7 +70,7 @@ struct __align__(16) Ctl {
   int32_t ticket;
   int32_t routed;              // every token's decision was seen
   int32_t last;
-  float4 amax[16];             // FP8: a column's largest |h| per epilogue warp
+  float4 amax[4];              // FP8: a token's largest |h| per epilogue warp, four tokens at a time
   int32_t sel_e[kSelfTokens * kMaxTopK];  // the block's own decisions
   float sel_w[kSelfTokens * kMaxTopK];
   DecideScratch decide;
@@ -780,8 +780,22 @@ DecodeSplits decode_splits(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I
   return c;
 }
 
-int64_t decode_counters(const DecodeSplits& cut, int32_t d, int32_t E, int32_t I, int32_t Is) {
-  return kCtrExpert + E + 1 + ceil_div(d, kMinColumns) + (cut.s1 > 1 || cut.s1s > 1 ? E * ceil_div(I, kRows) + ceil_div(Is, kRows) : 0);
+// Fewer tokens may be cut into more parts, so each count is the most that any call of up to n tokens
+// has. While the tokens' slots name an expert each (mk <= E), s1 * mk <= max(mk, 2 * kSms / gate/up tiles
+// of an expert), and s2 * mk, s2s * m <= max(mk, 4 * kSms / down tiles); past that the cut no longer changes.
+DecodeRows decode_rows(const DecodeSplits& c, int64_t n, int32_t d, int32_t k, int32_t I, int32_t Is, int32_t dtype) {
+  const int64_t nk = n * k;
+  if (dtype == MOE_F32) return DecodeRows{0, 0, nk, Is > 0 ? n : 0};
+  auto most = [](int64_t rows, int64_t parts, int64_t bound) {
+    const int64_t small = rows * kMaxParts < bound ? rows * kMaxParts : bound;
+    return rows * parts > small ? rows * parts : small;
+  };
+  const int64_t one = 2 * kSms / ceil_div(I, kRows), two = 4 * kSms / ceil_div(d, kColumns);
+  return DecodeRows{most(nk, c.s1, one), Is > 0 ? n * c.s1s : 0, most(nk, c.s2, two), Is > 0 ? most(n, c.s2s, two) : 0};
+}
+
+int64_t decode_counters(int32_t d, int32_t E, int32_t I, int32_t Is) {
+  return kCtrExpert + E + 1 + ceil_div(d, kMinColumns) + E * ceil_div(I, kRows) + ceil_div(Is, kRows);
 }
 
 bool decode_tc_supported() { return encode_fn() != nullptr; }

@@ -182,6 +182,12 @@ struct DecodeSplits {
   int32_t s1, per1, s1s, per1s, s2, per2, s2s, per2s;
 };
 DecodeSplits decode_splits(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I, int32_t Is, int32_t dtype);
+// Rows of the workspace's binary32 regions for a call of at most n tokens (n's cut is `c`): gate and up parts of
+// the routed and of the shared experts, down outputs of both.
+struct DecodeRows {
+  int64_t gu, gus, eo, es;
+};
+DecodeRows decode_rows(const DecodeSplits& c, int64_t n, int32_t d, int32_t k, int32_t I, int32_t Is, int32_t dtype);
 struct DecodeArgs {
   DecodeSplits cut;
   int32_t n, d, E, k, G, topk_group, score_fn, renorm, I, Is, dtype;
@@ -207,12 +213,11 @@ struct DecodeArgs {
   void* y;                   // [n, d]
   int32_t* counts;           // [E] or nullptr
   moe_diag* diag;            // or nullptr
-  int32_t* ctr;              // counters
-  void* clear;               // the status block and the counters: zeroed by the first launch
-  int32_t clear_bytes;
+  int32_t* ctr;              // counters, zeroed (and the status word) by the first launch
+  int32_t ctr_bytes;         // a multiple of 16
   moe_diag* status;
 };
-int64_t decode_counters(const DecodeSplits& cut, int32_t d, int32_t E, int32_t I, int32_t Is);  // counter words
+int64_t decode_counters(int32_t d, int32_t E, int32_t I, int32_t Is);  // counter words
 cudaError_t launch_decode_router(const DecodeArgs& a, cudaStream_t s);  // first: logits, x's codes, cleared counters
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t s);    // then the layer: binary32,
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s);      // or bf16 and FP8 experts
