@@ -232,10 +232,10 @@ moe_status moe_layer_forward(const moe_config* cfg, int64_t n, const void* x, co
  * Whole layer for the few tokens of a decode step, in two kernel launches (the
  * router's logits; everything else, set up while the first runs):
  * n <= MOE_DECODE_MAX_TOKENS, otherwise MOE_ERR_UNSUPPORTED. Arguments and
- * outputs are those of moe_layer_forward, every dtype and scoring; a capacity
- * is a property of a large batch and cfg->cap_policy must be MOE_CAP_NONE
- * (MOE_ERR_UNSUPPORTED otherwise, as for E * max(d, I) or n_shared * I of about
- * 2^31 and more).
+ * outputs are those of moe_layer_forward, every dtype and scoring; y may be x.
+ * A capacity is a property of a large batch: cfg->cap_policy must be
+ * MOE_CAP_NONE (MOE_ERR_UNSUPPORTED otherwise, as for E * max(d, I) or
+ * n_shared * I of about 2^31 and more).
  *   x_codes_opt [n, d], x_scale_bytes_opt [n, d / 128]: MOE_FP8 only, both or
  *   neither: the E4M3 tiles of x when the caller has them (moe_add_rmsnorm,
  *   moe_quantize_fp8); NULL: the call quantises x. The router always reads x.

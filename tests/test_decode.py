@@ -292,6 +292,98 @@ def test_workspace_shared_with_other_entry_points_in_turn():
     c.check(_oracle(w, host))
 
 
+@pytest.mark.gpu
+def test_calls_of_every_kind_at_once():
+    """Both kernels' forms and the large-batch layer overlap on streams, each call with its own workspace."""
+    kinds = [_get("tiny_f32", 40), _get("deepseek_v3_small", 64), _get("deepseek_v3_decode_small_fp8", 33), _get("mixtral_small", 1)]
+    want = [Call(w, dev)() for w, _, dev in kinds]
+    calls = [Call(w, dev) for w, _, dev in kinds]
+    big, _, bdev = _get("deepseek_v3_decode_small", 128)
+    bcfg, bw = H.cfg_for(big), _weights(bdev)
+    bws = torch.empty(moe.moe_workspace_size(bcfg, big.n), dtype=torch.uint8, device="cuda")
+    y0, y1 = (torch.empty(big.n, big.d_model, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    moe.moe_layer_forward(bcfg, big.n, bdev["x"], bw, y0, bws)
+    streams = [torch.cuda.Stream() for _ in range(len(calls) + 1)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                c()
+        with torch.cuda.stream(streams[-1]):
+            moe.moe_layer_forward(bcfg, big.n, bdev["x"], bw, y1, bws)
+    torch.cuda.synchronize()
+    for c, r in zip(calls, want):
+        assert moe.moe_sync_status(c.ws) == moe.MOE_OK
+        assert torch.equal(c.y, r.y) and torch.equal(c.idx, r.idx) and torch.equal(c.tw, r.tw)
+    assert torch.equal(y0, y1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,n", [("tiny_f32", 6), ("deepseek_v3_small", 2), ("deepseek_v3_decode_small_fp8", 24)])
+def test_captured_behind_a_copy_and_a_join(name, n):
+    """Inside a graph the call follows a copy (no kernel) on its own stream and a norm on another one."""
+    w, host, dev = _get(name, n)
+    c = Call(w, dev)
+    x, src, stale = dev["x"].clone(), dev["x"].clone(), torch.empty_like(dev["x"])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.copy_(src)
+        c(x)
+        x.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            moe.moe_add_rmsnorm(src, None, 1e-6, y=stale)
+            x.copy_(src)
+        torch.cuda.current_stream().wait_stream(side)
+        c(x)
+    src.copy_(W.device_inputs(w, seed=3, names=["x"])["x"])
+    for _ in range(3):
+        x.fill_(1.0)
+        graph.replay()
+    c.check(_oracle(w, dict(host, x=W.host_inputs(w, seed=3, names=["x"])["x"])))
+
+
+@pytest.mark.gpu
+def test_two_graphs_take_turns_on_one_workspace():
+    w, host, dev = _get("deepseek_v3_small", 48)
+    w1, host1, dev1 = _get("deepseek_v3_small", 2)
+    a, b = Call(w, dev), Call(w1, dev1)
+    b.ws = a.ws
+    graphs = []
+    for c in (a, b):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c()
+    for _ in range(4):
+        for g in graphs:
+            g.replay()
+    a.check(_oracle(w, host))
+    b.check(_oracle(w1, host1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,n", [("tiny_f32", 2), ("tiny_f32", 64), ("deepseek_v3_small", 1), ("deepseek_v3_small", 64),
+                                    ("deepseek_v3_decode_small_fp8", 40)])
+def test_y_in_the_place_of_x(name, n):
+    w, _, dev = _get(name, n)
+    a = Call(w, dev)()
+    for _ in range(5):
+        x = dev["x"].clone()
+        moe.moe_layer_decode(a.cfg, n, x, a.weights, x, a.ws)
+        assert torch.equal(x, a.y[:n])
+
+
+@pytest.mark.gpu
+def test_most_slots_with_given_codes():
+    w, host, dev = _get("fp8_ragged_small", 64, n_routed=40, top_k=32)
+    codes = torch.empty(64, w.d_model, dtype=torch.uint8, device="cuda")
+    sb = torch.empty(64, w.d_model // 128, dtype=torch.uint8, device="cuda")
+    moe.moe_quantize_fp8(dev["x"], codes, sb)
+    Call(w, dev)(x_codes=codes, x_scale_bytes=sb).check(_oracle(w, host))
+
+
 # ---- the step as it is used: residual add and norm, then the layer ---------------------
 
 

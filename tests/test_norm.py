@@ -214,3 +214,24 @@ def test_runs_in_a_graph_and_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     _check(x, r, w, 1e-6, y, s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(1, 7168), (300, 1024), (2000, 256), (400, 7168)])
+def test_calls_at_once_and_outputs_left_out(rows, cols):
+    x, r = _rand((rows, cols), torch.bfloat16, 16), _rand((rows, cols), torch.bfloat16, 17)
+    w = _rand((cols,), torch.bfloat16, 18)
+    y, s = torch.empty_like(x), torch.empty_like(x)
+    moe.moe_add_rmsnorm(x, w, 1e-6, y=y, residual=r, sum_out=s)
+    outs = [torch.empty_like(x) for _ in range(4)]
+    streams = [torch.cuda.Stream() for _ in outs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o, t in zip(outs, streams):
+            with torch.cuda.stream(t):
+                moe.moe_add_rmsnorm(x, w, 1e-6, y=o, residual=r)  # no sum_out
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, y) for o in outs)
+    z = x.clone()
+    moe.moe_add_rmsnorm(z, w, 1e-6, y=outs[0], residual=z, sum_out=outs[1])  # the same rows twice: s = 2 x
+    _check(z, z, w, 1e-6, outs[0], outs[1])
