@@ -180,6 +180,17 @@ def test_odd_shapes(kw, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name,kw", [
+    ("ragged_small", dict(n=3, d_model=2568, n_routed=2, top_k=2, moe_intermediate_size=9608, n_shared=0)),
+    ("fp8_ragged_small", dict(n=1, d_model=5120, n_routed=5, top_k=5, moe_intermediate_size=3840, n_shared=1)),
+])
+def test_long_tiles_in_halves(name, kw):
+    """A little over one turn of the SMs, with long k axes: gate/up tiles in two parts, down tiles in several."""
+    w, host, dev = _get(name, **kw)
+    Call(w, dev)().check(_oracle(w, host))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("groups,kept,experts", [(2, 1, 6), (16, 3, 64), (3, 2, 201)])
 def test_group_limits_off_32(groups, kept, experts):
     w, host, dev = _get("deepseek_v3_small", 19, n_group=groups, topk_group=kept, n_routed=experts, top_k=3)

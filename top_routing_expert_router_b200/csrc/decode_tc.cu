@@ -46,14 +46,20 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSfCol0 = 256;           // after two pairs of accumulators of at most 64 columns
 constexpr uint32_t kSfCols = 12;            // per slot: D0's rows, D1's rows, the tokens
 constexpr size_t kSmemLimit = 232448;
-// Few experts (a token or two) leave fewer tiles than SMs, and one SM draws at most about 65 GB/s, so
-// tiles are cut along k: into as many parts as keep the parts within one turn of the SMs (two turns for
-// down tiles), of at least what the ring holds, kMinPart k blocks; tiles of nearly one (two) turns are halved. A part of a
-// gate/up tile costs a round trip through L2; down tiles join their parts in the combine. Measured at one
-// token: 16 gate/up tiles 81 us whole, 40.5 in nine parts; 96 tiles 66.8 us whole, 76.4 halved; 128 tiles
-// and 252 down tiles (DeepSeek-V3 shapes, FP8) 79 us with both halved, 83 with either whole; 32 down tiles
-// of 7.3 MB (Mixtral shapes) 201 us whole, 130 in nine parts.
-constexpr int kSms = 148, kMinPart = 6, kMaxParts = 16;
+// Few experts leave few tiles for the SMs, and one SM draws at most about 65 GB/s, so tiles are cut along
+// k. A part of a gate/up tile costs a round trip through L2; down tiles join their parts in the combine.
+// Gate/up: as many parts as keep them within one turn of the SMs, each of at least what the ring holds,
+// kMinPart k blocks; from three quarters of a turn to eight turns, halves (past one turn only of tiles
+// of twice kLongPart k blocks or more: 264 tiles of 32 blocks take 85 us whole, 88 halved).
+// Down: parts within two turns, of at least kMinPart blocks, or three turns in at most kWideParts parts of
+// twice kMinPart (64 tiles of 44 blocks: 65 us in four parts, 68 in six); halves from one to two turns.
+// Measured, one token unless said: 16 gate/up tiles 81 us whole, 40.5 in nine parts; 96 tiles 66.8 us
+// whole, 76.4 halved; 128 tiles and 252 down tiles (DeepSeek-V3 shapes, FP8) 79 us with both halved, 83 with
+// either whole; 224 gate/up tiles (Mixtral shapes) 132 us whole, 121 halved, 131 in three; its 32 down
+// tiles of 7.3 MB 200 us whole, 121 in nine parts; 160 and 80 tiles (d = 4096, five experts of 4096) 111 us
+// whole and in three, 94 halved and in five; 896 and 128 tiles (Mixtral, 4 tokens) 337 us whole and
+// halved, 321 halved and in three.
+constexpr int kSms = 148, kMinPart = 6, kMaxParts = 16, kLongPart = 20, kWideParts = 9;
 
 struct __align__(16) Ctl {
   uint64_t full[kMaxStages];   // weights' and tokens' arrivals
@@ -772,16 +778,24 @@ DecodeSplits decode_splits(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I
   const int64_t tiles1 = active * ceil_div(I, kRows), tiles1s = ceil_div(Is, kRows);
   const int64_t tiles2 = (active + (Is > 0)) * ceil_div(d, kColumns);
   const bool fp8 = dtype == MOE_FP8;
-  split_k(tiles1 >= kSms * 3 / 4 && tiles1 < kSms ? 2 : kSms / tiles1, ceil_div(d, ke), fp8, &c.s1, &c.per1);
-  split_k(tiles1s > 0 ? kSms / tiles1s : 1, ceil_div(d, ke), fp8, &c.s1s, &c.per1s);
-  const int64_t parts2 = tiles2 >= kSms && tiles2 < 2 * kSms ? 2 : 2 * kSms / tiles2;
-  split_k(parts2, ceil_div(I, ke), fp8, &c.s2, &c.per2);
-  split_k(parts2, ceil_div(Is, ke), fp8, &c.s2s, &c.per2s);
+  const int64_t kb1 = ceil_div(d, ke);
+  const bool halved = tiles1 >= kSms * 3 / 4 && (tiles1 < kSms || (tiles1 < 8 * kSms && kb1 >= 2 * kLongPart));
+  split_k(halved ? 2 : kSms / tiles1, kb1, fp8, &c.s1, &c.per1);
+  split_k(tiles1s > 0 ? kSms / tiles1s : 1, kb1, fp8, &c.s1s, &c.per1s);
+  auto parts2 = [&](int64_t nkb) {
+    const int64_t two = tiles2 >= kSms && tiles2 < 2 * kSms ? 2 : 2 * kSms / tiles2;
+    int64_t three = 3 * kSms / tiles2;
+    if (three > nkb / (2 * kMinPart)) three = nkb / (2 * kMinPart);
+    if (three > kWideParts) three = kWideParts;
+    return two > three ? two : three;
+  };
+  split_k(parts2(ceil_div(I, ke)), ceil_div(I, ke), fp8, &c.s2, &c.per2);
+  split_k(parts2(ceil_div(Is, ke)), ceil_div(Is, ke), fp8, &c.s2s, &c.per2s);
   return c;
 }
 
 // Fewer tokens may be cut into more parts, so each count is the most that any call of up to n tokens
-// has. While the tokens' slots name an expert each (mk <= E), s1 * mk <= max(mk, 2 * kSms / gate/up tiles
+// has. While the tokens' slots name an expert each (mk <= E), s1 * mk <= max(mk, 16 * kSms / gate/up tiles
 // of an expert), and s2 * mk, s2s * m <= max(mk, 4 * kSms / down tiles); past that the cut no longer changes.
 DecodeRows decode_rows(const DecodeSplits& c, int64_t n, int32_t d, int32_t k, int32_t I, int32_t Is, int32_t dtype) {
   const int64_t nk = n * k;
@@ -790,7 +804,7 @@ DecodeRows decode_rows(const DecodeSplits& c, int64_t n, int32_t d, int32_t k, i
     const int64_t small = rows * kMaxParts < bound ? rows * kMaxParts : bound;
     return rows * parts > small ? rows * parts : small;
   };
-  const int64_t one = 2 * kSms / ceil_div(I, kRows), two = 4 * kSms / ceil_div(d, kColumns);
+  const int64_t one = 16 * kSms / ceil_div(I, kRows), two = 4 * kSms / ceil_div(d, kColumns);
   return DecodeRows{most(nk, c.s1, one), Is > 0 ? n * c.s1s : 0, most(nk, c.s2, two), Is > 0 ? most(n, c.s2s, two) : 0};
 }
 
