@@ -243,10 +243,10 @@ moe_status moe_layer_forward(const moe_config* cfg, int64_t n, const void* x, co
  * indices are those of the binary64 definition with no second pass (diag's
  * overflowed, dropped and refined_* are 0); a token whose x is not finite has
  * NaN logits and takes the lowest experts; expert products accumulate in
- * binary32; the intermediate is rounded to the activation type (then to E4M3
- * for MOE_FP8) as in moe_expert_ffn; expert outputs stay binary32 and are
- * rounded once, as y. The results differ from moe_layer_forward's by those
- * roundings.
+ * binary32; the intermediate is kept to 16 bits of its significand for MOE_BF16
+ * and is rounded to bf16 and E4M3 for MOE_FP8, as in moe_expert_ffn; expert
+ * outputs stay binary32 and are rounded once, as y. The results differ from
+ * moe_layer_forward's by those roundings.
  * ws: moe_workspace_size() bytes of this n or of any larger one; two calls that
  * overlap on the GPU need two workspaces (graphs replayed at once too). Waits
  * between the launch's own blocks are bounded (2 s, then MOE_ERR_TIMEOUT in the

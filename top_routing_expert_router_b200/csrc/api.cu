@@ -22,7 +22,7 @@ struct Plan {
   size_t diag, logits, rq, rc, ranking, capg, blk, idx, w, counts, offsets, perm, dest, xperm, h, eo, shh, sh, shoff, sched;
   size_t xq, sfx, hq, sfh, xsq, sfxs, hsq, sfhs;  // FP8 experts: E4M3 activations and their scale blocks
   size_t sfb, sfbs;  // FP8 SM-pair GEMMs: B scale blocks (routed, shared experts)
-  size_t dctr, dlog, dgu, deo, des, dhs, dhss, dxs;  // moe_layer_decode: counters, binary64 logits, binary32 parts and outputs, scale bytes
+  size_t dctr, dlog, dgu, deo, des, dhs, dhss, dxs, dh, dhh;  // moe_layer_decode: counters, binary64 logits, binary32 parts and outputs, scale bytes, h in two bf16 rows
   size_t ep_off;  // expert parallelism: receive offsets of the rank's own experts
   size_t total;
   bool batched;   // the two-kernel router queues its undecided tokens for launch_refine (rq, rc reserved)
@@ -157,6 +157,8 @@ Plan make_plan(const moe_config& c, int64_t n, int32_t ep_world = 0, int64_t ep_
     p.dxs = take(fp8 ? (size_t)few * (d / 128) : 0);
     p.dhs = take(fp8 ? (size_t)few * c.top_k * (I / 128) : 0);
     p.dhss = take(fp8 ? (size_t)few * (Is / 128) : 0);
+    p.dh = take(c.dtype == MOE_BF16 ? (size_t)2 * few * c.top_k * I * 2 : 0);
+    p.dhh = take(c.dtype == MOE_BF16 ? (size_t)2 * few * Is * 2 : 0);
   }
   p.total = off;
   return p;
@@ -1019,8 +1021,8 @@ moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, con
   a.logits = c.at<double>(c.p.dlog);
   a.topk_idx = topk_idx_opt ? topk_idx_opt : c.at<int32_t>(c.p.idx);
   a.topk_w = topk_w_opt ? topk_w_opt : c.at<float>(c.p.w);
-  a.h = fp8 ? c.at<void>(c.p.hq) : c.at<void>(c.p.h);
-  a.hs = fp8 ? c.at<void>(c.p.hsq) : c.at<void>(c.p.shh);
+  a.h = c.at<void>(fp8 ? c.p.hq : f.dtype == MOE_BF16 ? c.p.dh : c.p.h);
+  a.hs = c.at<void>(fp8 ? c.p.hsq : f.dtype == MOE_BF16 ? c.p.dhh : c.p.shh);
   a.h_scale = c.at<uint8_t>(c.p.dhs);
   a.hs_scale = c.at<uint8_t>(c.p.dhss);
   a.gu = c.at<float>(c.p.dgu);

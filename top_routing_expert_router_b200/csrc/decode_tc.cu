@@ -5,7 +5,9 @@
 // 128 hidden columns; 256 output columns of a down matrix) times N token columns, N = the tokens
 // rounded up to 16. D0 and D1, 128 x N binary32 each in TMEM, hold a token per column, so a gate/up
 // tile multiplies every token of the batch and stores the columns of the expert's tokens: no row is
-// gathered and no operand is padded to 128 rows. At N <= 64 the MMAs take under a tenth of the time
+// gathered and no operand is padded to 128 rows. bf16 experts keep h as the sum of two bf16 rows (16 bits:
+// y then carries one rounding, where one bf16 row made its error 1.4 times as large); the two are columns
+// side by side of a down tile's MMA, added in the epilogue, and the weights are read once. At N <= 64 the MMAs take under a tenth of the time
 // the weights take to arrive; the kernel is bound by HBM.
 //
 // One CTA per SM, 384 threads, warp-specialised:
@@ -43,7 +45,7 @@ constexpr int kCombineTokens = 8;           // tokens of a combine unit
 constexpr int kMaxStages = 8;
 constexpr int kQueue = 4;                   // tiles published ahead of the slowest reader
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSfCol0 = 256;           // after two pairs of accumulators of at most 64 columns
+constexpr uint32_t kSfCol0 = 256;           // FP8: after two pairs of accumulators of at most 64 columns (bf16: of 128)
 constexpr uint32_t kSfCols = 12;            // per slot: D0's rows, D1's rows, the tokens
 constexpr size_t kSmemLimit = 232448;
 // Few experts leave few tiles for the SMs, and one SM draws at most about 65 GB/s, so tiles are cut along
@@ -224,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                                                                const __grid_constant__ DecodeArgs a,
                                                                const __grid_constant__ TcShape sh) {
   constexpr int KE = FP8 ? 128 : 64;  // elements of k per stage
+  constexpr int HR = FP8 ? 1 : 2;     // rows of h for a token's slot
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + sh.ctl_off);
@@ -231,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
   uint16_t* slot_r = reinterpret_cast<uint16_t*>(slot_w + a.n * a.k);     // [n * k] expert output rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int N = sh.n_cols, stages = sh.stages;
+  const uint32_t dcols = (uint32_t)(N * HR);  // columns of an accumulator
   const int shared = a.Is > 0;
   const int tiles1 = (a.I + kRows - 1) / kRows, tiles1s = (a.Is + kRows - 1) / kRows;
   const int tiles2 = (a.d + kColumns - 1) / kColumns;
@@ -364,9 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         const int buf = i & 1;
         if (!(ok = wait(&ctl->tmem_empty[buf], ((uint32_t)(i >> 1) & 1u) ^ 1u))) break;
         fence_after();
-        const uint32_t d0 = tmem_base + (uint32_t)(buf * 2 * N), d1 = d0 + (uint32_t)N;
+        const uint32_t d0 = tmem_base + buf * 2 * dcols, d1 = d0 + dcols;
         const bool two = two_blocks(tl);
-        const int cols = columns(tl);
+        const int cols = columns(tl) * (tl.down ? HR : 1);
         for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
           if (!(ok = wait(&ctl->full[stage], phase))) break;
           fence_after();
@@ -478,11 +482,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
         __syncwarp();
         if (lane == 0) {
-          mbar_expect_tx(&ctl->full[stage], (uint32_t)cols * kKB);
-          if (tl.down && !s)
-            for (int c = 0; c < cols; c += 16) tma_load_2d(sb + c * kKB, m, &ctl->full[stage], kb * KE, tl.row0 + c);
-          else
-            tma_load_2d(sb, m, &ctl->full[stage], kb * KE, 0);
+          const int parts = tl.down ? HR : 1, apart = s ? a.n : a.n * a.k;  // rows of h between a slot's two
+          mbar_expect_tx(&ctl->full[stage], (uint32_t)(parts * cols) * kKB);
+          for (int p = 0; p < parts; ++p) {
+            if (tl.down && !s)
+              for (int c = 0; c < cols; c += 16)
+                tma_load_2d(sb + (p * cols + c) * kKB, m, &ctl->full[stage], kb * KE, p * apart + tl.row0 + c);
+            else
+              tma_load_2d(sb + p * cols * kKB, m, &ctl->full[stage], kb * KE, p * apart);
+          }
         }
         if (++stage == stages) stage = 0, phase ^= 1u;
       }
@@ -558,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
           if (lane == 0) mbar_arrive(&ctl->tile_empty[q]);
           if (++q == kQueue) q = 0, qphase ^= 1u;
           fence_after();
-          const uint32_t d0 = tmem_base + ((uint32_t)(rw * 32) << 16) + (uint32_t)(buf * 2 * N), d1 = d0 + (uint32_t)N;
+          const uint32_t d0 = tmem_base + ((uint32_t)(rw * 32) << 16) + buf * 2 * dcols, d1 = d0 + dcols;
           const bool s = tl.e == a.E;
           auto release = [&] {  // the accumulators are read
             fence_before();
@@ -645,10 +653,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 named_sync<2, 128>();  // amax is the next columns'
               } else {
                 bf16* h = static_cast<bf16*>(s ? a.hs : a.h);
+                bf16* h2 = h + (int64_t)(s ? a.n : a.n * a.k) * tl.Ie;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   if (!((mine >> j) & 1u)) continue;
-                  if (c < tl.Ie) h[(int64_t)row * tl.Ie + c] = from_f32<bf16>(g[j]);
+                  const bf16 top = from_f32<bf16>(g[j]);
+                  const float rest = fabsf(to_f32(top)) < INFINITY ? g[j] - to_f32(top) : 0.0f;
+                  if (c < tl.Ie) {
+                    h[(int64_t)row * tl.Ie + c] = top;
+                    h2[(int64_t)row * tl.Ie + c] = from_f32<bf16>(rest);
+                  }
                   ++row;
                 }
               }
@@ -664,6 +678,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             for (int t0 = 0; t0 < tl.m; t0 += 4) {
               float v0[4], v1[4];
               tmem_ld4x2(d0 + (uint32_t)t0, (two ? d1 : d0) + (uint32_t)t0, v0, v1);
+              if constexpr (HR == 2) {
+                float u0[4], u1[4];
+                const uint32_t at = (uint32_t)(columns(tl) + t0);
+                tmem_ld4x2(d0 + at, (two ? d1 : d0) + at, u0, u1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v0[j] += u0[j], v1[j] += u1[j];
+              }
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 if (t0 + j >= tl.m) break;
@@ -818,7 +839,8 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s) {
   const bool fp8 = a.dtype == MOE_FP8;
   TcShape sh{};
   sh.n_cols = (int32_t)align_up(a.n, 16);
-  sh.stage_bytes = 2 * kABytes + sh.n_cols * kKB;
+  const int halves = fp8 ? 1 : 2;  // rows of h for a token's slot
+  sh.stage_bytes = 2 * kABytes + halves * sh.n_cols * kKB;
   const int64_t slots = align_up((int64_t)a.n * a.k * 6, 16);
   const int64_t sf = fp8 ? 3 * kSfBytes : 0;  // scale words, outside the stages to keep those on 1024 bytes
   const int64_t fit = ((int64_t)kSmemLimit - 1024 - slots - (int64_t)sizeof(Ctl)) / (sh.stage_bytes + sf);
@@ -832,13 +854,13 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t s) {
   const int64_t E = a.E, nk = (int64_t)a.n * a.k;
   bool ok = make_map(&m.gate, fp8, a.w_gate, E * a.I, a.d, kRows) && make_map(&m.up, fp8, a.w_up, E * a.I, a.d, kRows) &&
             make_map(&m.down, fp8, a.w_down, E * a.d, a.I, kRows) &&
-            make_map(&m.x, fp8, fp8 ? a.xq : a.x, a.n, a.d, sh.n_cols) && make_map(&m.h, fp8, a.h, nk, a.I, 16);
+            make_map(&m.x, fp8, fp8 ? a.xq : a.x, a.n, a.d, sh.n_cols) && make_map(&m.h, fp8, a.h, halves * nk, a.I, 16);
   m.sgate = m.sup = m.gate;
   m.sdown = m.down;
   m.hs = m.h;
   if (a.Is > 0)
     ok = ok && make_map(&m.sgate, fp8, a.ws_gate, a.Is, a.d, kRows) && make_map(&m.sup, fp8, a.ws_up, a.Is, a.d, kRows) &&
-         make_map(&m.sdown, fp8, a.ws_down, a.d, a.Is, kRows) && make_map(&m.hs, fp8, a.hs, a.n, a.Is, sh.n_cols);
+         make_map(&m.sdown, fp8, a.ws_down, a.d, a.Is, kRows) && make_map(&m.hs, fp8, a.hs, halves * a.n, a.Is, sh.n_cols);
   if (!ok) return cudaErrorInvalidValue;
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);

@@ -203,8 +203,8 @@ struct DecodeArgs {
   double* logits;            // [n, E]
   int32_t* topk_idx;         // [n, k]
   float* topk_w;             // [n, k]
-  void* h;                   // [n * k, I] act, or E4M3 codes
-  void* hs;                  // [n, Is]
+  void* h;                   // [n * k, I] binary32 or E4M3 codes; bf16: [2, n * k, I], a value's two parts
+  void* hs;                  // [n, Is], likewise
   uint8_t* h_scale;          // FP8: [n * k, I / 128]
   uint8_t* hs_scale;         // FP8: [n, Is / 128]
   float* gu;                 // tiles in parts: [n * k, s1, 2, I] gate and up sums, then [n, s1s, 2, Is]
