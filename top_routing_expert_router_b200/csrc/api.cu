@@ -147,8 +147,7 @@ Plan make_plan(const moe_config& c, int64_t n, int32_t ep_world = 0, int64_t ep_
   // for moe_layer_decode of at most n tokens, whose needs grow with its tokens (decode_rows)
   const int64_t few = ep || c.cap_policy != MOE_CAP_NONE ? 0 : n < MOE_DECODE_MAX_TOKENS ? n : MOE_DECODE_MAX_TOKENS;
   if (few > 0) {
-    const DecodeSplits cut = decode_splits(few, c.d_model, c.n_routed, c.top_k, c.moe_intermediate_size, (int32_t)Is, c.dtype);
-    const DecodeRows rows = decode_rows(cut, few, c.d_model, c.top_k, c.moe_intermediate_size, (int32_t)Is, c.dtype);
+    const DecodeRows rows = decode_rows(few, c.d_model, c.n_routed, c.top_k, c.moe_intermediate_size, (int32_t)Is, c.dtype);
     p.dctr = take((size_t)decode_counters(c.d_model, c.n_routed, c.moe_intermediate_size, (int32_t)Is) * 4);
     p.dlog = take((size_t)few * c.n_routed * 8);
     p.dgu = take((size_t)2 * (rows.gu * I + rows.gus * Is) * 4);

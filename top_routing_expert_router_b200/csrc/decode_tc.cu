@@ -50,9 +50,11 @@ constexpr uint32_t kSfCols = 12;            // per slot: D0's rows, D1's rows, t
 constexpr size_t kSmemLimit = 232448;
 // Few experts leave few tiles for the SMs, and one SM draws at most about 65 GB/s, so tiles are cut along
 // k. A part of a gate/up tile costs a round trip through L2; down tiles join their parts in the combine.
-// Gate/up: as many parts as keep them within one turn of the SMs, each of at least what the ring holds,
-// kMinPart k blocks; from three quarters of a turn to eight turns, halves (past one turn only of tiles
-// of twice kLongPart k blocks or more: 264 tiles of 32 blocks take 85 us whole, 88 halved).
+// Gate/up: at most as many parts as keep them within one turn of the SMs, each of at least what the ring
+// holds, kMinPart k blocks; from three quarters of a turn to eight turns, halves (past one turn only of tiles
+// of twice kLongPart k blocks or more: 264 tiles of 32 blocks take 85 us whole, 88 halved). Fewer for many
+// tokens, whose parts one block joins (gate_parts): 55 tokens and 2 shared tiles of 110 blocks 145 us in 16
+// parts, 87 in four; 59 tokens and 18 shared tiles of 17 blocks 89 us in two, 72 whole.
 // Down: parts within two turns, of at least kMinPart blocks, or three turns in at most kWideParts parts of
 // twice kMinPart (64 tiles of 44 blocks: 65 us in four parts, 68 in six); halves from one to two turns.
 // Measured, one token unless said: 16 gate/up tiles 81 us whole, 40.5 in nine parts; 96 tiles 66.8 us
@@ -612,17 +614,30 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
               if (!mine) continue;
               float g[4], u[4];
               if (tl.parts > 1) {
-                int from = row;
+                // the four tokens' parts, four at a time: 32 loads in flight (a token after the other took
+                // about a microsecond each: 59 tokens of 75 experts 108 us, 90 so)
+                const float* o[4];
+                bool on[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   g[j] = u[j] = 0.0f;
-                  if (!((mine >> j) & 1u) || c >= tl.Ie) continue;
-                  const float* o = part + (int64_t)from++ * tl.parts * 2 * tl.Ie + c;
-#pragma unroll 8
-                  for (int p = 0; p < tl.parts; ++p) {
-                    g[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie);
-                    u[j] += __ldcg(o + (int64_t)p * 2 * tl.Ie + tl.Ie);
-                  }
+                  on[j] = ((mine >> j) & 1u) && c < tl.Ie;
+                  o[j] = part + (int64_t)(row + __popc(mine & ((1u << j) - 1u))) * tl.parts * 2 * tl.Ie + c;
+                }
+                for (int p0 = 0; p0 < tl.parts; p0 += 4) {
+                  float vg[4][4], vu[4][4];
+#pragma unroll
+                  for (int p = 0; p < 4; ++p)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                      const bool in = on[j] && p0 + p < tl.parts;
+                      vg[p][j] = in ? __ldcg(o[j] + (int64_t)(p0 + p) * 2 * tl.Ie) : 0.0f;
+                      vu[p][j] = in ? __ldcg(o[j] + (int64_t)(p0 + p) * 2 * tl.Ie + tl.Ie) : 0.0f;
+                    }
+#pragma unroll
+                  for (int p = 0; p < 4; ++p)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) g[j] += vg[p][j], u[j] += vu[p][j];
                 }
               } else {
                 tmem_ld4x2(d0 + (uint32_t)t0, d1 + (uint32_t)t0, g, u);
@@ -791,6 +806,28 @@ void split_k(int64_t p, int64_t nkb, bool fp8, int32_t* parts, int32_t* per) {
 
 }  // namespace
 
+// Most parts of a gate/up tile when there are `tiles` of nkb blocks.
+static int64_t gate_parts_limit(int64_t tiles, int64_t nkb) {
+  if (tiles <= 0) return 1;
+  const bool halved = tiles >= kSms * 3 / 4 && (tiles < kSms || (tiles < 8 * kSms && nkb >= 2 * kLongPart));
+  int64_t p = halved ? 2 : kSms / tiles;
+  if (p > nkb / kMinPart) p = nkb / kMinPart;
+  if (p > kMaxParts) p = kMaxParts;
+  return p > 1 ? p : 1;
+}
+
+// Of up to `limit` parts the number that is done first, for a tile of `tokens` rows: in quarters of a
+// microsecond, a block of k takes 2, a join 6 and, by fours of tokens and of parts, 4.
+static int64_t gate_parts(int64_t limit, int64_t nkb, int64_t tokens) {
+  const int64_t fours = ceil_div(tokens, 4);
+  int64_t best = 1, least = 2 * nkb;
+  for (int64_t p = 2; p <= limit; ++p) {
+    const int64_t cost = 2 * nkb / p + 6 + fours * (p > 4 ? p : 4);
+    if (cost <= least) best = p, least = cost;
+  }
+  return best;
+}
+
 DecodeSplits decode_splits(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I, int32_t Is, int32_t dtype) {
   DecodeSplits c{1, 0, 1, 0, 1, 0, 1, 0};
   if (dtype == MOE_F32) return c;
@@ -800,9 +837,8 @@ DecodeSplits decode_splits(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I
   const int64_t tiles2 = (active + (Is > 0)) * ceil_div(d, kColumns);
   const bool fp8 = dtype == MOE_FP8;
   const int64_t kb1 = ceil_div(d, ke);
-  const bool halved = tiles1 >= kSms * 3 / 4 && (tiles1 < kSms || (tiles1 < 8 * kSms && kb1 >= 2 * kLongPart));
-  split_k(halved ? 2 : kSms / tiles1, kb1, fp8, &c.s1, &c.per1);
-  split_k(tiles1s > 0 ? kSms / tiles1s : 1, kb1, fp8, &c.s1s, &c.per1s);
+  split_k(gate_parts(gate_parts_limit(tiles1, kb1), kb1, ceil_div(n * k, active)), kb1, fp8, &c.s1, &c.per1);
+  split_k(gate_parts(gate_parts_limit(tiles1s, kb1), kb1, n), kb1, fp8, &c.s1s, &c.per1s);
   auto parts2 = [&](int64_t nkb) {
     const int64_t two = tiles2 >= kSms && tiles2 < 2 * kSms ? 2 : 2 * kSms / tiles2;
     int64_t three = 3 * kSms / tiles2;
@@ -817,16 +853,19 @@ DecodeSplits decode_splits(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I
 
 // Fewer tokens may be cut into more parts, so each count is the most that any call of up to n tokens
 // has. While the tokens' slots name an expert each (mk <= E), s1 * mk <= max(mk, 16 * kSms / gate/up tiles
-// of an expert), and s2 * mk, s2s * m <= max(mk, 4 * kSms / down tiles); past that the cut no longer changes.
-DecodeRows decode_rows(const DecodeSplits& c, int64_t n, int32_t d, int32_t k, int32_t I, int32_t Is, int32_t dtype) {
-  const int64_t nk = n * k;
+// of an expert) and s2 * mk, s2s * m <= max(mk, 4 * kSms / down tiles); past that the limits no longer change.
+DecodeRows decode_rows(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I, int32_t Is, int32_t dtype) {
+  const int64_t nk = n * k, kb1 = ceil_div(d, dtype == MOE_FP8 ? 128 : 64);
   if (dtype == MOE_F32) return DecodeRows{0, 0, nk, Is > 0 ? n : 0};
+  const DecodeSplits c = decode_splits(n, d, E, k, I, Is, dtype);
   auto most = [](int64_t rows, int64_t parts, int64_t bound) {
     const int64_t small = rows * kMaxParts < bound ? rows * kMaxParts : bound;
     return rows * parts > small ? rows * parts : small;
   };
-  const int64_t one = 16 * kSms / ceil_div(I, kRows), two = 4 * kSms / ceil_div(d, kColumns);
-  return DecodeRows{most(nk, c.s1, one), Is > 0 ? n * c.s1s : 0, most(nk, c.s2, two), Is > 0 ? most(n, c.s2s, two) : 0};
+  const int64_t tiles1 = ceil_div(I, kRows), tiles1s = ceil_div(Is, kRows), tiles2 = ceil_div(d, kColumns);
+  return DecodeRows{most(nk, gate_parts_limit((nk < E ? nk : E) * tiles1, kb1), 16 * kSms / tiles1),
+                    Is > 0 ? n * gate_parts_limit(tiles1s, kb1) : 0, most(nk, c.s2, 4 * kSms / tiles2),
+                    Is > 0 ? most(n, c.s2s, 4 * kSms / tiles2) : 0};
 }
 
 int64_t decode_counters(int32_t d, int32_t E, int32_t I, int32_t Is) {

@@ -182,12 +182,12 @@ struct DecodeSplits {
   int32_t s1, per1, s1s, per1s, s2, per2, s2s, per2s;
 };
 DecodeSplits decode_splits(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I, int32_t Is, int32_t dtype);
-// Rows of the workspace's binary32 regions for a call of at most n tokens (n's cut is `c`): gate and up parts of
+// Rows of the workspace's binary32 regions for a call of at most n tokens: gate and up parts of
 // the routed and of the shared experts, down outputs of both.
 struct DecodeRows {
   int64_t gu, gus, eo, es;
 };
-DecodeRows decode_rows(const DecodeSplits& c, int64_t n, int32_t d, int32_t k, int32_t I, int32_t Is, int32_t dtype);
+DecodeRows decode_rows(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I, int32_t Is, int32_t dtype);
 struct DecodeArgs {
   DecodeSplits cut;
   int32_t n, d, E, k, G, topk_group, score_fn, renorm, I, Is, dtype;
