@@ -4,7 +4,8 @@ against the fp64 oracle, and the calls the documentation allows.
 Tolerances of y are the layer parity tests' (2e-2 for bf16 and FP8, 1e-4 for binary32, relative to the larger of the
 element and its row's rms). In bf16 the error is that of h and of y, each rounded by at most 2^-8 of itself: over a
 row of sums that is a standard deviation of 2^-8 / sqrt(3) = 0.0023 of the rms from h, the largest of 64 x 512 such
-values lying near 4.3 of them (0.0097), plus 2^-8 (0.0039) from y: 0.0136. In binary32 the same with 2^-24 per
+values lying near 4.3 of them (0.0097), plus 2^-8 (0.0039) from y: 0.0136. (That is with h in one bf16 row, as in
+FP8's tiles; bf16 experts keep 16 bits of it, which leaves y's part.) In binary32 the same with 2^-24 per
 rounding, of which a sum of 7168 terms takes at most 7168 in a chain: 4.3e-4 at worst, about sqrt(7168) * 2^-24 =
 5e-6 as roundings go; the largest sum below has 512 terms (3e-5 at worst). Gates are sums in binary64 rounded once
 to binary32: 2^-24, and 2^-22 allows for the two exponentials' own errors."""

@@ -614,8 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
               if (!mine) continue;
               float g[4], u[4];
               if (tl.parts > 1) {
-                // the four tokens' parts, four at a time: 32 loads in flight (a token after the other took
-                // about a microsecond each: 59 tokens of 75 experts 108 us, 90 so)
+                // the four tokens' parts, four at a time: 32 loads in flight (a token after the other took about
+                // a microsecond each: 29 tokens, five experts and a shared one in four parts 70 us, 54 so)
                 const float* o[4];
                 bool on[4];
 #pragma unroll
