@@ -7,7 +7,7 @@ row of sums that is a standard deviation of 2^-8 / sqrt(3) = 0.0023 of the rms f
 values lying near 4.3 of them (0.0097), plus 2^-8 (0.0039) from y: 0.0136. (That is with h in one bf16 row, as in
 FP8's tiles; bf16 experts keep 16 bits of it, which leaves y's part.) In binary32 the same with 2^-24 per
 rounding, of which a sum of 7168 terms takes at most 7168 in a chain: 4.3e-4 at worst, about sqrt(7168) * 2^-24 =
-5e-6 as roundings go; the largest sum below has 512 terms (3e-5 at worst). Gates are sums in binary64 rounded once
+5e-6 as roundings go; the largest sum below has 1032 terms (6.2e-5 at worst). Gates are sums in binary64 rounded once
 to binary32: 2^-24, and 2^-22 allows for the two exponentials' own errors."""
 import ctypes
 
@@ -165,6 +165,21 @@ def _get(name, n, **kw):
 def test_layer_parity(name, n):
     w, host, dev = _get(name, n)
     Call(w, dev)().check(_oracle(w, host))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,n", [("deepseek_v3_small", 16), ("deepseek_v3_small", 64), ("ragged_small", 7), ("mixtral_small", 33)])
+def test_bf16_carries_one_rounding(name, n):
+    """y is off by its own rounding (2^-8 of itself) and by h's 16 bits: 2^-16 of each term. Of 512 normal terms the
+    magnitudes sum to 0.64 * 512 / sqrt(512) = 14.4 times the sum's rms, so 14.4 * 2^-16 = 2.2e-4 of it at worst; 2^-11
+    (4.9e-4) leaves the binary32 sums (512 * 2^-24 = 3.1e-5 of the magnitudes' 14.4: 4.4e-4 if every one erred its way,
+    2e-5 as roundings go) their part."""
+    w, host, dev = _get(name, n)
+    r, c = _oracle(w, host), Call(w, dev)()
+    keep = ~r["exempt"]
+    y, want = H.as_f64(c.y)[:n][keep], r["y"][keep]
+    rms = np.sqrt(np.mean(want * want, axis=1, keepdims=True))
+    assert (np.abs(y - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -11 * rms).all()
 
 
 @pytest.mark.gpu
