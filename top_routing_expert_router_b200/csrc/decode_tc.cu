@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         if (!ok) atomicExch(&ctl->abort, 1);
       }
       if (!all(ok)) break;
+      __syncwarp();  // lane 0's acquire comes before every lane's reads of h's scale bytes: a shuffle orders no memory
       const bool s = tl.e == a.E;
       const CUtensorMap* m = !tl.down ? &maps.x : (s ? &maps.hs : &maps.h);
       const int cols = columns(tl), nkb = (tl.down ? tl.Ie : a.d) / KE;  // FP8: scale bytes per row
