@@ -5,8 +5,8 @@
 //   codes, scale_bytes = the 1 x 128 E4M3 quantisation of y as rounded to T,
 // so that the codes are those moe_quantize_fp8 gives for y. The norm reads s
 // before its rounding to T: one rounding per output. A row's sum of squares is
-// held in binary32; one that overflows (|s| above about 1e17) is taken again of
-// s * 2^-80, under which no row of finite values overflows and eps vanishes.
+// held in binary32; where the mean square overflows (|s| above about 1e17) it is taken
+// again of s * 2^-80, under which no row of finite values overflows (norm_of).
 //
 // A row lives in registers between its loads and its stores, as the raw vectors of x and r (8
 // elements, vector v of the row in thread v % TPR), so each is read once and all of a row's loads
@@ -82,7 +82,7 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
-// y = s * scale * (inv + inv_lo) (* w): scale is 1, or 2^-80 for a row whose squares overflow.
+// y = s * scale * (inv + inv_lo) (* w): scale is 1, or 2^-8 for a row whose mean square overflows.
 struct Norm {
   float scale, inv, inv_lo;
 };
@@ -93,21 +93,24 @@ struct Norm {
 // differ from the exact norm rounded once, against 51 % with three rounded products; of 29 million
 // bf16 values 223 do, nearly all by the rounding of s = x + r to binary32 where x and r are far apart.
 // (The sum of squares with its remainder carried along would leave 202, and takes 4 to 18 % longer.)
-__device__ __forceinline__ Norm inverse_rms(float ss, const NormArgs& n, float eps, float scale) {
+__device__ __forceinline__ Norm inverse_rms(float ss, const NormArgs& n, float eps) {
   const float q = ss * n.inv_cols, q_lo = fmaf(-q, (float)n.cols, ss) * n.inv_cols;
   const float a = q + eps, z = a - q;
   const float a_lo = ((q - (a - z)) + (eps - z)) + q_lo;
   const float inv = rsqrtf(a), p = inv * inv;
   const float r = fmaf(-a, p, 1.0f) - a * fmaf(inv, inv, -p) - a_lo * p;
   // (r means nothing where a is infinite, or so small that p overflows)
-  return Norm{scale, inv, a >= 0x1p-120f && a < INFINITY ? 0.5f * inv * r : 0.0f};
+  return Norm{1.0f, inv, a >= 0x1p-120f && a < INFINITY ? 0.5f * inv * r : 0.0f};
 }
 
 // The row's Norm. square_sum(scale, store) sums (s * scale)^2 over the row (and stores sum_out).
+// Where the sum overflows, the root is that of s * 2^-80 (eps vanishes beside it): its inverse lies in
+// [2^-48, 2^24], and of the 2^-80 that takes it back 2^-72 go to it and 2^-8 to s, so that neither leaves
+// binary32's range: 2^-80 times s alone took the digits of values below 2^-46 beside others above 1e17.
 template <int TPR, int ROWS, typename Sum>
 __device__ __forceinline__ Norm norm_of(const NormArgs& a, bool live, int local, int tid, int* overflow, Sum square_sum) {
   const float ss = square_sum(1.0f, true);
-  Norm n = inverse_rms(ss, a, a.eps, 1.0f);
+  Norm n = inverse_rms(ss, a, a.eps);
   // the block's rows take the second sum together: it holds a barrier
   const bool mine = live && !(ss < INFINITY);
   bool big = mine;
@@ -120,7 +123,10 @@ __device__ __forceinline__ Norm norm_of(const NormArgs& a, bool live, int local,
   }
   if (big) {
     const float ss2 = square_sum(0x1p-80f, false);
-    if (mine) n = inverse_rms(ss2, a, 0.0f, 0x1p-80f);
+    if (mine) {
+      n = inverse_rms(ss2, a, 0.0f);
+      n = Norm{0x1p-8f, n.inv * 0x1p-72f, n.inv_lo * 0x1p-72f};
+    }
   }
   return n;
 }
@@ -184,9 +190,10 @@ __device__ __forceinline__ void finish_vector(const NormArgs& a, int64_t row, in
 // ---- a row per block turn ----------------------------------------------------------
 // Blocks an SM must hold, which bounds the registers: 768 threads (85 registers) for bf16 and 512 for
 // binary32 (128; without the bound the compiler took 138, and 16384 x 7168 went from 301 to 370 us).
-// Rows of a warp or two are quicker with as many registers as the compiler likes.
+// Rows of a warp or two are quicker with more: bf16 with the 128 that let an SM hold four blocks (20000 x 1024 with a
+// residual: 31 us; 36 with the 148 that the compiler would take), binary32 with as many as the compiler likes.
 template <typename T, int TPR>
-constexpr int kMinBlocks = TPR < 128 || TPR > 256 ? 1 : (sizeof(T) == 2 ? 768 : 512) / TPR;
+constexpr int kMinBlocks = TPR < 128 ? (sizeof(T) == 2 ? 4 : 1) : TPR > 256 ? 1 : (sizeof(T) == 2 ? 768 : 512) / TPR;
 
 template <typename T, int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kMinBlocks<T, TPR>) add_rmsnorm_kernel(NormArgs a) {
