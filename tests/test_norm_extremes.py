@@ -47,3 +47,16 @@ def test_small_values_beside_huge_ones(dtype, rows, cols):
         y = torch.full_like(x, float("nan"))
         moe.moe_add_rmsnorm(x, gain, 1e-6, y=y)
         _check(x, gain, 1e-6, y)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("eps", [1e34, 1e37, 3.4e38])
+@pytest.mark.parametrize("rows,cols", [(2, 200), (9, 512), (300, 256), (300, 8192)])
+def test_eps_beside_squares_that_overflow(dtype, eps, rows, cols):
+    """eps counts however large: beside a sum of squares past binary32, and where its own sum with the mean is."""
+    g = torch.Generator().manual_seed(rows + cols)
+    x = torch.randn(rows, cols, generator=g) * 2.0 ** torch.linspace(40, 63.9, rows)[:, None]
+    x = x.to(dtype).cuda()
+    y = torch.full_like(x, float("nan"))
+    moe.moe_add_rmsnorm(x, None, eps, y=y)
+    _check(x, None, eps, y)

@@ -104,7 +104,7 @@ __device__ __forceinline__ Norm inverse_rms(float ss, const NormArgs& n, float e
 }
 
 // The row's Norm. square_sum(scale, store) sums (s * scale)^2 over the row (and stores sum_out).
-// Where the sum overflows, the root is that of s * 2^-80 (eps vanishes beside it): its inverse lies in
+// Where the mean square with eps overflows, the root is that of s * 2^-80 and eps * 2^-160: its inverse lies in
 // [2^-48, 2^24], and of the 2^-80 that takes it back 2^-72 go to it and 2^-8 to s, so that neither leaves
 // binary32's range: 2^-80 times s alone took the digits of values below 2^-46 beside others above 1e17.
 template <int TPR, int ROWS, typename Sum>
@@ -112,7 +112,7 @@ __device__ __forceinline__ Norm norm_of(const NormArgs& a, bool live, int local,
   const float ss = square_sum(1.0f, true);
   Norm n = inverse_rms(ss, a, a.eps);
   // the block's rows take the second sum together: it holds a barrier
-  const bool mine = live && !(ss < INFINITY);
+  const bool mine = live && !(n.inv > 0.0f);  // an infinite root, or no number
   bool big = mine;
   if constexpr (TPR < 128 && TPR > 32) {
     if (tid == 0) overflow[local] = mine;
@@ -124,7 +124,7 @@ __device__ __forceinline__ Norm norm_of(const NormArgs& a, bool live, int local,
   if (big) {
     const float ss2 = square_sum(0x1p-80f, false);
     if (mine) {
-      n = inverse_rms(ss2, a, 0.0f);
+      n = inverse_rms(ss2, a, a.eps * 0x1p-80f * 0x1p-80f);
       n = Norm{0x1p-8f, n.inv * 0x1p-72f, n.inv_lo * 0x1p-72f};
     }
   }
