@@ -60,3 +60,19 @@ def test_eps_beside_squares_that_overflow(dtype, eps, rows, cols):
     y = torch.full_like(x, float("nan"))
     moe.moe_add_rmsnorm(x, None, eps, y=y)
     _check(x, None, eps, y)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("eps", [1e-45, 1e-40, 1e-36, 1e-29])
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_tiny_eps_beside_squares_that_vanish(dtype, eps, rows, cols):
+    """Rows of values whose squares are below binary32's range, of some within it, and of zeros."""
+    g = torch.Generator().manual_seed(rows + cols)
+    x = torch.randn(rows, cols, generator=g) * 2.0 ** torch.linspace(-90, -40, rows)[:, None]
+    x[rows // 2] = 0
+    w = (1 + torch.randn(cols, generator=g)).to(dtype).cuda()
+    x = x.to(dtype).cuda()
+    y = torch.full_like(x, float("nan"))
+    moe.moe_add_rmsnorm(x, w, eps, y=y)
+    _check(x, w, eps, y)
+    assert (y[rows // 2] == 0).all()

@@ -5,8 +5,8 @@
 //   codes, scale_bytes = the 1 x 128 E4M3 quantisation of y as rounded to T,
 // so that the codes are those moe_quantize_fp8 gives for y. The norm reads s
 // before its rounding to T: one rounding per output. A row's sum of squares is
-// held in binary32; where the mean square overflows (|s| above about 1e17) it is taken
-// again of s * 2^-80, under which no row of finite values overflows (norm_of).
+// held in binary32; where the mean square overflows (|s| above about 1e17), or it and eps
+// nearly vanish (below 2^-100), it is taken again of s times a power of two (norm_of).
 //
 // A row lives in registers between its loads and its stores, as the raw vectors of x and r (8
 // elements, vector v of the row in thread v % TPR), so each is read once and all of a row's loads
@@ -107,12 +107,14 @@ __device__ __forceinline__ Norm inverse_rms(float ss, const NormArgs& n, float e
 // Where the mean square with eps overflows, the root is that of s * 2^-80 and eps * 2^-160: its inverse lies in
 // [2^-48, 2^24], and of the 2^-80 that takes it back 2^-72 go to it and 2^-8 to s, so that neither leaves
 // binary32's range: 2^-80 times s alone took the digits of values below 2^-46 beside others above 1e17.
+// Where mean square and eps are below 2^-100, the squares vanish or lose digits: the root is that of s * 2^80 and
+// eps * 2^160, its inverse below 2^-5, and all of the 2^80 goes to it.
 template <int TPR, int ROWS, typename Sum>
 __device__ __forceinline__ Norm norm_of(const NormArgs& a, bool live, int local, int tid, int* overflow, Sum square_sum) {
   const float ss = square_sum(1.0f, true);
   Norm n = inverse_rms(ss, a, a.eps);
   // the block's rows take the second sum together: it holds a barrier
-  const bool mine = live && !(n.inv > 0.0f);  // an infinite root, or no number
+  const bool tiny = n.inv > 0x1p50f, mine = live && (tiny || !(n.inv > 0.0f));  // (an infinite root, or no number)
   bool big = mine;
   if constexpr (TPR < 128 && TPR > 32) {
     if (tid == 0) overflow[local] = mine;
@@ -122,10 +124,12 @@ __device__ __forceinline__ Norm norm_of(const NormArgs& a, bool live, int local,
     for (int i = 0; i < ROWS; ++i) big |= overflow[i] != 0;
   }
   if (big) {
-    const float ss2 = square_sum(0x1p-80f, false);
+    const float f = tiny ? 0x1p80f : 0x1p-80f;
+    const float ss2 = square_sum(f, false);
     if (mine) {
-      n = inverse_rms(ss2, a, a.eps * 0x1p-80f * 0x1p-80f);
-      n = Norm{0x1p-8f, n.inv * 0x1p-72f, n.inv_lo * 0x1p-72f};
+      n = inverse_rms(ss2, a, a.eps * f * f);
+      const float back = tiny ? 0x1p80f : 0x1p-72f;
+      n = Norm{tiny ? 1.0f : 0x1p-8f, n.inv * back, n.inv_lo * back};
     }
   }
   return n;
