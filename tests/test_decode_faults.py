@@ -38,3 +38,47 @@ def test_scale_bytes_of_an_earlier_call_are_not_seen(n):
         c(loud if i % 2 else dev["x"])
         assert torch.equal(c.y, want[i % 2])
     assert moe.moe_sync_status(c.ws) == moe.MOE_OK
+
+
+# ---- types -------------------------------------------------------------------------
+
+
+def _tensors(dtype, **kw):
+    cfg = moe.make_config(d_model=512, n_routed=32, top_k=4, moe_intermediate_size=256, dtype=dtype)
+    act = torch.float32 if dtype == "f32" else torch.bfloat16
+    t = dict(x=torch.zeros(4, 512, dtype=act), y=torch.zeros(4, 512, dtype=act), topk_idx=torch.zeros(4, 4, dtype=torch.int32),
+             topk_w=torch.zeros(4, 4), counts=torch.zeros(32, dtype=torch.int32), diag=torch.zeros(8, dtype=torch.int32))
+    if dtype == "fp8":
+        t.update(x_codes=torch.zeros(4, 512, dtype=torch.uint8), x_scale_bytes=torch.zeros(4, 4, dtype=torch.uint8))
+    return cfg, {**t, **kw}
+
+
+def _refusal(dtype, **kw):
+    """What the binding says to host tensors, which it refuses at last for that."""
+    cfg, t = _tensors(dtype, **kw)
+    with pytest.raises(ValueError) as e:
+        moe.moe_layer_decode(cfg, 4, t.pop("x"), moe.moe_weights(), t.pop("y"), torch.zeros(16, dtype=torch.uint8), **t)
+    return str(e.value)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+def test_binding_refuses_other_types(dtype):
+    assert "CUDA" in _refusal(dtype)
+    wrong = torch.bfloat16 if dtype == "f32" else torch.float32
+    for name, t in [("x", torch.zeros(8, 512, dtype=wrong)), ("x", torch.zeros(8, 512, dtype=torch.float16)),
+                    ("y", torch.zeros(8, 512, dtype=wrong)), ("topk_idx", torch.zeros(4, 4, dtype=torch.int64)),
+                    ("topk_idx", torch.zeros(4, 4)), ("topk_w", torch.zeros(4, 4, dtype=torch.float64)),
+                    ("counts", torch.zeros(32, dtype=torch.int64)), ("diag", torch.zeros(8, dtype=torch.int64))]:
+        assert f"{name} is {t.dtype}" in _refusal(dtype, **{name: t})
+    if dtype == "fp8":
+        for name, kind in (("x_codes", torch.float8_e4m3fn), ("x_scale_bytes", torch.float8_e8m0fnu)):
+            _, t = _tensors(dtype)
+            assert "CUDA" in _refusal(dtype, **{name: t[name].view(kind)})
+            assert f"{name} is" in _refusal(dtype, **{name: t[name].to(torch.int32)})
+            assert f"{name} is" in _refusal(dtype, **{name: t[name].view(torch.float8_e5m2)})
+
+
+def test_binding_refuses_what_is_too_small_or_strided():
+    assert "y has" in _refusal("bf16", y=torch.zeros(3, 512, dtype=torch.bfloat16))
+    assert "x has" in _refusal("bf16", x=torch.zeros(512, 4, dtype=torch.bfloat16).T)
+    assert "topk_w has" in _refusal("f32", topk_w=torch.zeros(4, 3))

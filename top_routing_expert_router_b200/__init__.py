@@ -208,18 +208,29 @@ def moe_layer_forward(cfg, n, x, weights, y, ws, topk_idx=None, topk_w=None, cou
 def moe_layer_decode(cfg, n, x, weights, y, ws, topk_idx=None, topk_w=None, counts=None, diag=None, x_codes=None,
                      x_scale_bytes=None, stream=None):
     """moe_layer_forward for n <= MOE_DECODE_MAX_TOKENS tokens in two launches; x_codes and x_scale_bytes are x's E4M3
-    tiles (MOE_FP8) when the caller has them. Every tensor is contiguous and on ws's device."""
+    tiles (MOE_FP8; torch.uint8, or the 8-bit float types they stand for) when the caller has them. x and y are
+    torch.float32 (MOE_F32) or torch.bfloat16, topk_idx, counts and diag torch.int32, topk_w torch.float32. Every tensor
+    is contiguous and on ws's device."""
+    import torch
+
     where = "moe_layer_decode"
     index, d, slots = ws.get_device(), cfg.d_model, 4 * n * cfg.top_k
-    row = n * d * (4 if cfg.dtype == MOE_F32 else 2)
-    for t, need in ((x, row), (y, row), (topk_idx, slots), (topk_w, slots), (counts, 4 * cfg.n_routed), (diag, 32),
-                    (x_codes, n * d), (x_scale_bytes, n * (d // 128)), (ws, 0)):
+    act, width = (torch.float32, 4) if cfg.dtype == MOE_F32 else (torch.bfloat16, 2)
+    row = n * d * width
+    for name, t, need, kind in (("x", x, row, act), ("y", y, row, act), ("topk_idx", topk_idx, slots, torch.int32),
+                                ("topk_w", topk_w, slots, torch.float32), ("counts", counts, 4 * cfg.n_routed, torch.int32),
+                                ("diag", diag, 32, torch.int32), ("x_codes", x_codes, n * d, torch.float8_e4m3fn),
+                                ("x_scale_bytes", x_scale_bytes, n * (d // 128), torch.float8_e8m0fnu), ("ws", ws, 0, None)):
         if t is None:
             continue
-        if index < 0 or t.get_device() != index:
-            raise ValueError(f"{where}: every tensor must be on the same CUDA device")
+        if kind is not None and t.dtype != kind and not (kind.itemsize == 1 and t.dtype == torch.uint8):
+            raise ValueError(f"{where}: {name} is {t.dtype} where {kind} is needed")
         if t.nbytes < need or not t.is_contiguous():
-            raise ValueError(f"{where}: a tensor of {t.nbytes} bytes where {need} contiguous ones are needed")
+            raise ValueError(f"{where}: {name} has {t.nbytes} bytes where {need} contiguous ones are needed")
+        if t.get_device() != index:
+            raise ValueError(f"{where}: every tensor must be on the same CUDA device")
+    if index < 0:
+        raise ValueError(f"{where}: the tensors must be on a CUDA device")
     _call_on(index, _lib.moe_layer_decode, where,
              (ctypes.byref(cfg), n, _ptr(x), _ptr(x_codes), _ptr(x_scale_bytes), ctypes.byref(weights), _ptr(y), _ptr(topk_idx),
               _ptr(topk_w), _ptr(counts), _ptr(diag), ws.data_ptr(), ws.nbytes), stream)
