@@ -79,9 +79,11 @@
  *     the rows per expert allow them); these exist for tuning and tests, and
  *     results are identical up to floating-point summation order.
  *     MOE_EP_TIMEOUT_MS bounds the expert-parallel barrier wait (see below).
- *     MOE_TEST_STALL=1 withholds one pipeline stage of the bf16 expert GEMM so
- *     that its bounded wait runs out and MOE_ERR_TIMEOUT is reported (a test of
- *     the failure path; never set it otherwise).
+ *     MOE_TEST_STALL=1 withholds one pipeline stage of the bf16 expert GEMM, and
+ *     in moe_layer_decode the word that an expert's hidden rows are finished (2:
+ *     that a token is decided), so that a bounded wait runs out and
+ *     MOE_ERR_TIMEOUT is reported (a test of the failure path; never set it
+ *     otherwise).
  *     MOE_TEST_NO_TENSOR_MAPS=1 makes the bf16 tensor-core GEMMs report every
  *     shape as unsupported (a test of that path; never set it otherwise).
  *   - bf16 matrix products run on the tcgen05 tensor cores only: a shape or

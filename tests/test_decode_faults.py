@@ -82,3 +82,53 @@ def test_binding_refuses_what_is_too_small_or_strided():
     assert "y has" in _refusal("bf16", y=torch.zeros(3, 512, dtype=torch.bfloat16))
     assert "x has" in _refusal("bf16", x=torch.zeros(512, 4, dtype=torch.bfloat16).T)
     assert "topk_w has" in _refusal("f32", topk_w=torch.zeros(4, 3))
+
+
+# ---- waits that run out ------------------------------------------------------------
+
+
+BIG = dict(d_model=4096, n_routed=16, top_k=4, moe_intermediate_size=2048)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("stall", ["1", "2"])
+@pytest.mark.parametrize("name,n,kw", [
+    ("tiny_f32", 5, {}), ("tiny_f32", 64, dict(d_model=1024, moe_intermediate_size=1024)),
+    ("ragged_small", 7, {}), ("ragged_small", 3, BIG), ("ragged_small", 64, BIG),
+    ("fp8_ragged_small", 7, {}), ("fp8_ragged_small", 3, BIG), ("fp8_ragged_small", 40, BIG),
+])
+def test_abandoned_call_leaves_the_gpu_as_it_was(name, n, kw, stall, monkeypatch):
+    """An expert's hidden rows are never reported finished (2: a token never decided): the waits for them end at their
+    limit, the call leaves MOE_ERR_TIMEOUT, and neither the call right behind it nor the next one on its workspace
+    sees anything of it."""
+    w = W.get(name, n=n, **kw)
+    dev = W.device_inputs(w)
+    want, bad, good = Call(w, dev)(), Call(w, dev), Call(w, dev)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        monkeypatch.setenv("MOE_TEST_STALL", stall)
+        bad()
+        monkeypatch.delenv("MOE_TEST_STALL")
+        good()
+        assert moe.moe_sync_status(bad.ws) == moe.MOE_ERR_TIMEOUT
+        assert moe.moe_sync_status(bad.ws) == moe.MOE_OK  # reading clears the word
+        assert moe.moe_sync_status(good.ws) == moe.MOE_OK
+        assert torch.equal(good.y, want.y) and torch.equal(good.idx, want.idx)
+        assert (bad.y[n:] == 7).all()
+        bad()
+        assert moe.moe_sync_status(bad.ws) == moe.MOE_OK
+        assert torch.equal(bad.y, want.y) and torch.equal(bad.idx, want.idx)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,n", [("tiny_f32", 1), ("ragged_small", 1), ("fp8_ragged_small", 2)])
+def test_abandoned_call_of_tokens_that_every_block_decides(name, n, monkeypatch):
+    w = W.get(name, n=n)
+    dev = W.device_inputs(w)
+    want, c = Call(w, dev)(), Call(w, dev)
+    monkeypatch.setenv("MOE_TEST_STALL", "1")
+    c()
+    assert moe.moe_sync_status(c.ws) == moe.MOE_ERR_TIMEOUT
+    monkeypatch.delenv("MOE_TEST_STALL")
+    c()
+    assert moe.moe_sync_status(c.ws) == moe.MOE_OK and torch.equal(c.y, want.y)

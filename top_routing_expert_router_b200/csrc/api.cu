@@ -1034,6 +1034,9 @@ moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, con
   a.status = c.status();
   const bool tensor = f.dtype != MOE_F32;
   if (tensor && !decode_tc_supported()) return MOE_ERR_UNSUPPORTED;
+  const char* stall = getenv("MOE_TEST_STALL");  // waits that never end, so that they run out (a test of that path)
+  a.test_stall = stall && (stall[0] == '1' || stall[0] == '2') ? stall[0] - '0' : 0;
+  a.wait_cycles = a.test_stall ? kDecodeTestWaitCycles : kDecodeWaitCycles;
   a.ctr_bytes = (int32_t)align_up(decode_counters(a.d, a.E, a.I, a.Is) * 4, 16);
   MOE_CUDA(launch_decode_router(a, c.s));
   return cuda_status(tensor ? launch_decode_tc(a, c.s) : launch_decode_simt(a, c.s));

@@ -9,7 +9,7 @@
 // tiles (shared experts first), down tiles. A unit waits only for units that were claimed before
 // it, so some block is running each of them and every wait ends, whatever share of the grid is
 // resident: no cooperative launch, and calls on several streams may overlap on the GPU. Waits are
-// bounded all the same (kDecodeTimeoutCycles).
+// bounded all the same (kDecodeWaitCycles).
 //
 // Sums are deterministic: no floating-point atomics; whichever block adds the expert rows of a
 // column range takes them in slot order.
@@ -24,10 +24,6 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-// Limit of any single wait: 2 s at the highest clock. (Reading the SM's clock takes a few cycles, where
-// %globaltimer takes long enough to delay a wait that ends meanwhile.)
-constexpr long long kDecodeTimeoutCycles = 4000000000ll;
-
 // Counter words (zeroed before the launch).
 enum {
   kCtrAbort = 0,
@@ -54,15 +50,16 @@ __device__ __forceinline__ int add_release(int32_t* p, int v) {
   return old;
 }
 
-// One thread waits until *p >= target. False once the call is abandoned.
-__device__ __noinline__ inline bool wait_counter(const int32_t* p, int target, int32_t* ctr, moe_diag* status) {
+// One thread waits until *p >= target. False once the call is abandoned. (The limit is read off the SM's clock, which
+// takes a few cycles; %globaltimer takes long enough to delay a wait that ends meanwhile.)
+__device__ __noinline__ inline bool wait_counter(const int32_t* p, int target, int32_t* ctr, moe_diag* status, int64_t limit) {
   if (ld_acquire(p) >= target) return true;
   const long long t0 = clock64();
   for (uint32_t it = 1;; ++it) {
     if (ld_acquire(p) >= target) return true;
     if ((it & 63u) == 0) {
       if (ld_acquire(ctr + kCtrAbort)) return false;
-      if (clock64() - t0 > kDecodeTimeoutCycles) {
+      if (clock64() - t0 > limit) {
         atomicExch(ctr + kCtrAbort, 1);
         set_status(status, MOE_ERR_TIMEOUT);
         return false;

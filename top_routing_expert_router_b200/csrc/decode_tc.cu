@@ -77,6 +77,7 @@ struct __align__(16) Ctl {
   int32_t tile[kQueue];
   uint32_t tmem_base;
   int32_t abort;
+  uint32_t armed[2];           // stages that the weight and the token warp have armed, written as they leave
   int32_t ticket;
   int32_t routed;              // every token's decision was seen
   int32_t last;
@@ -100,7 +101,7 @@ struct TcShape {
   int32_t ctl_off;
 };
 
-__device__ __noinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* ctr, moe_diag* st) {
+__device__ __noinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* ctr, moe_diag* st, int64_t limit) {
   const uint32_t b = smem_u32(bar);
   if (mbar_try(b, parity)) return true;
   const long long t0 = clock64();
@@ -108,7 +109,7 @@ __device__ __noinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, Ctl* ctl,
     if (mbar_try(b, parity)) return true;
     if ((it & 255u) == 0) {
       if (*reinterpret_cast<volatile int32_t*>(&ctl->abort)) return false;
-      if (clock64() - t0 > kDecodeTimeoutCycles) {
+      if (clock64() - t0 > limit) {
         atomicExch(&ctl->abort, 1);
         atomicExch(ctr + kCtrAbort, 1);
         set_status(st, MOE_ERR_TIMEOUT);
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
   wait_for_earlier_kernels();
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_try(smem_u32(bar), parity) || mbar_wait(bar, parity, ctl, a.ctr, a.status);
+    return mbar_try(smem_u32(bar), parity) || mbar_wait(bar, parity, ctl, a.ctr, a.status, a.wait_cycles);
   };
   const int count1 = tiles1 * a.cut.s1, count1s = tiles1s * a.cut.s1s;  // an expert's gate/up tiles, parts counted
   const int count2 = tiles2 * a.cut.s2, count2s = shared * tiles2 * a.cut.s2s;
@@ -349,9 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
           if (++stage == stages) stage = 0, phase ^= 1u;
         }
       }
-      if (!ok)  // let the copies in flight land
-        for (uint32_t s = 0; s < (uint32_t)stages; ++s)
-          if (armed > s) mbar_drain(&ctl->full[s], ((armed - 1 - s) / stages) & 1u);
+      ctl->armed[0] = armed;
     }
   } else if (warp == 1) {
     // ================= MMA =================
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
       int stage = 0, q = 0, i = 0;
       uint32_t phase = 0, qphase = 0;
       [[maybe_unused]] uint32_t sf_slot = 0;  // FP8: scale words of four k blocks, two slots in turn
-      bool ok = true, issued = false;
+      bool ok = true;
       for (;; ++i) {
         if (!(ok = wait(&ctl->tile_full[q], qphase))) break;
         const int t = ctl->tile[q];
@@ -401,22 +400,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
               if (two) mma_bf16(d1, a1 + (uint64_t)(2 * k), b + (uint64_t)(2 * k), id, ((kb - tl.kb0) | k) != 0);
             }
           }
-          issued = true;
           mma_commit(&ctl->empty[stage]);
           if (++stage == stages) stage = 0, phase ^= 1u;
         }
         if (!ok) break;
         mma_commit(&ctl->tmem_full[buf]);
       }
-      if (!ok && issued) {
-        mma_commit(&ctl->drain);
-        mbar_drain(&ctl->drain, 0);
-      }
     }
   } else if (warp == 2) {
     // ================= tokens (and FP8 scale words) =================
     int stage = 0, q = 0;
-    uint32_t phase = 0, qphase = 0;
+    uint32_t phase = 0, qphase = 0, armed = 0;
     auto all = [&](bool v) { return __shfl_sync(kFull, (int)v, 0) != 0; };
     for (;;) {
       if (!all(lane != 0 || wait(&ctl->tile_full[q], qphase))) break;
@@ -429,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
       if (++q == kQueue) q = 0, qphase ^= 1u;
       bool ok = true;
       if (lane == 0) {
-        if (tl.down) ok = wait_counter(a.ctr + kCtrExpert + tl.e, tl.e == a.E ? tiles1s : tiles1, a.ctr, a.status);  // its h
+        if (tl.down) ok = wait_counter(a.ctr + kCtrExpert + tl.e, tl.e == a.E ? tiles1s : tiles1, a.ctr, a.status, a.wait_cycles);  // its h
         fence_async_global();
         if (!ok) atomicExch(&ctl->abort, 1);
       }
@@ -487,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         if (lane == 0) {
           const int parts = tl.down ? HR : 1, apart = s ? a.n : a.n * a.k;  // rows of h between a slot's two
           mbar_expect_tx(&ctl->full[stage], (uint32_t)(parts * cols) * kKB);
+          ++armed;
           for (int p = 0; p < parts; ++p) {
             if (tl.down && !s)
               for (int c = 0; c < cols; c += 16)
@@ -499,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
       }
       if (!ok) break;
     }
+    if (lane == 0) ctl->armed[1] = armed;
   } else if (warp >= 4) {
     // ================= router =================
     const int tid = threadIdx.x - 128, rw = warp - 4;
@@ -518,10 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         const int t = ctl->ticket;
         if (t >= a.n) break;
         decide_token(a, t, bias, &ctl->decide, tid, sync, a.topk_idx + t * a.k, a.topk_w + t * a.k);
-        if (tid == 0) add_release(a.ctr + kCtrTokenDone, 1);  // decide_token ends with a barrier
+        // (decide_token ends with a barrier)
+        if (tid == 0 && (a.test_stall != 2 || t != 0)) add_release(a.ctr + kCtrTokenDone, 1);
       }
       if (tid == 0) {
-        ctl->routed = wait_counter(a.ctr + kCtrTokenDone, a.n, a.ctr, a.status);
+        ctl->routed = wait_counter(a.ctr + kCtrTokenDone, a.n, a.ctr, a.status, a.wait_cycles);
         if (!ctl->routed) atomicExch(&ctl->abort, 1);
       }
       sync();
@@ -684,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
               }
             }
             if (tl.parts == 1) release();
-            count(a.ctr + kCtrExpert + tl.e, INT_MAX);
+            if (a.test_stall != 1 || tl.r0 != 0) count(a.ctr + kCtrExpert + tl.e, INT_MAX);
             continue;
           }
           {
@@ -718,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
           u = unit;
           unit += gridDim.x;
           bool done = true;
-          if (r == 0) done = wait_counter(a.ctr + kCtrExpert + a.E + 1 + u % tiles2, parts, a.ctr, a.status);
+          if (r == 0) done = wait_counter(a.ctr + kCtrExpert + a.E + 1 + u % tiles2, parts, a.ctr, a.status, a.wait_cycles);
           if (!named_and<2, 128>(done)) break;
         }
         const int c = u % tiles2 * kColumns + 4 * (r & 63);
@@ -766,6 +763,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
   fence_before();
   __syncthreads();
   fence_after();
+  if (ctl->abort) {
+    // An abandoned call: wherever each warp stopped, nothing that writes this block's shared or tensor memory outlives
+    // it. Of a stage's two arrivals (weights, tokens) one may be missing: the other's copies land in a phase that its
+    // substitute completes. (A stage is armed again only after both came, so the two counts differ by one at most.)
+    if (threadIdx.x == 0)
+      for (int s = 0; s < stages; ++s) {
+        auto fills = [&](uint32_t armed) { return armed > (uint32_t)s ? (armed - 1 - s) / stages + 1 : 0u; };
+        const uint32_t w = fills(ctl->armed[0]), t = fills(ctl->armed[1]), most = w > t ? w : t;
+        if (w != t) mbar_arrive(&ctl->full[s]);
+        if (most) mbar_drain(&ctl->full[s], (most - 1) & 1u);
+      }
+    if (threadIdx.x == 32) {  // the thread that issued the MMAs
+      mma_commit(&ctl->drain);
+      mbar_drain(&ctl->drain, 0);
+    }
+  }
   if (warp == 1) {
     __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");

@@ -188,6 +188,8 @@ struct DecodeRows {
   int64_t gu, gus, eo, es;
 };
 DecodeRows decode_rows(int64_t n, int32_t d, int32_t E, int32_t k, int32_t I, int32_t Is, int32_t dtype);
+constexpr int64_t kDecodeWaitCycles = 4000000000ll;  // 2 s at the highest clock
+constexpr int64_t kDecodeTestWaitCycles = 100000ll;   // 50 us under injected stalls: others are then still at work
 struct DecodeArgs {
   DecodeSplits cut;
   int32_t n, d, E, k, G, topk_group, score_fn, renorm, I, Is, dtype;
@@ -215,6 +217,8 @@ struct DecodeArgs {
   moe_diag* diag;            // or nullptr
   int32_t* ctr;              // counters, zeroed (and the status word) by the first launch
   int32_t ctr_bytes;         // a multiple of 16
+  int32_t test_stall;        // fault injection: 1 = an expert's first gate/up tile is never reported finished, 2 = nor is a decision
+  int64_t wait_cycles;       // limit of any single wait, in SM clocks
   moe_diag* status;
 };
 int64_t decode_counters(int32_t d, int32_t E, int32_t I, int32_t Is);  // counter words
