@@ -167,7 +167,9 @@ typedef struct {
 } moe_diag;
 
 /*
- * Workspace bytes needed by any entry point for this cfg and token count n.
+ * Workspace bytes needed by any entry point for this cfg and token count n
+ * (moe_layer_decode's regions included, which are most of it at few tokens).
+ * The figure belongs to this version of the library: ask for it, keep none.
  * Returns MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED for a bad cfg.
  */
 moe_status moe_workspace_size(const moe_config* cfg, int64_t n, size_t* bytes);
@@ -233,7 +235,8 @@ moe_status moe_layer_forward(const moe_config* cfg, int64_t n, const void* x, co
 /*
  * Whole layer for the few tokens of a decode step, in two kernel launches (the
  * router's logits; everything else, set up while the first runs):
- * n <= MOE_DECODE_MAX_TOKENS, otherwise MOE_ERR_UNSUPPORTED. Arguments and
+ * n <= MOE_DECODE_MAX_TOKENS, otherwise MOE_ERR_UNSUPPORTED; up to there it was
+ * the faster call at every size measured (1.06 to 26 times). Arguments and
  * outputs are those of moe_layer_forward, every dtype and scoring; y may be x.
  * A capacity is a property of a large batch: cfg->cap_policy must be
  * MOE_CAP_NONE (MOE_ERR_UNSUPPORTED otherwise, as for E * max(d, I) or
@@ -278,7 +281,10 @@ moe_status moe_quantize_fp8(const void* x, int64_t rows, int32_t cols, uint8_t* 
  * transformer block in front of the layer. The pages name the norm and the
  * residual stream without a formula; per row, in binary32:
  *   s = x + residual (s = x without one),   sum_out = s rounded to dtype,
- *   y = s * weight / sqrt(mean(s^2) + eps), rounded once to dtype,
+ *   y = s * weight / sqrt(mean(s^2) + eps), within 31 * 2^-24 of itself for the
+ *   roundings of s and of the sum of squares, then rounded to dtype; rows whose
+ *   squares leave binary32's range keep this, and so does any eps (a value that
+ *   sinks below 2^-126 before the weight has steps of 2^-149 there),
  *   codes, scale_bytes = what moe_quantize_fp8 gives for y (for MOE_F32, the
  *   same tiles of the binary32 y).
  *   in : x [rows, cols], residual [rows, cols] or NULL, weight [cols] or NULL

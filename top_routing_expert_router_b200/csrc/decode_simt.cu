@@ -7,9 +7,12 @@
 // elements 4 l .. 4 l + 3 of each 128-wide chunk, and the 8 x tokens sums meet at the end of the rows
 // by halving exchanges. Weights come through a ring of cp.async copies, each slot written and read by
 // one thread, so no barrier guards them; a tile's first chunks are on their way before the tile in
-// front of it is summed up. Token rows come through L1. Up to eight tokens of an expert this is bound
-// by HBM; more are taken in passes over the tile (from L2) and bound by the FMA rate: 64 tokens need
-// 64 FMAs for each four bytes, 2.9 times as long as the bytes take.
+// front of it is summed up. Token rows come through L1. With many tiles and up to eight tokens an expert
+// this is bound by HBM (80 experts of 1536 x 5120, 24 tokens: 1134 us for 1021); more tokens are taken in
+// passes over the tile (from L2) and bound by the FMA rate: 64 tokens need 64 FMAs for each four bytes,
+// 2.9 times as long as the bytes take. Tiles are not cut along k, so a few of them leave most of the GPU
+// waiting (58 tokens, six experts of 3040 x 216, 24 down tiles for 296 blocks: 174 us for 7; four tokens, 44
+// experts of 96 x 2800: 46 for 7).
 #include "decode.cuh"
 
 namespace moe {

@@ -4,7 +4,7 @@
 //   sum_out = round_T(s),  y = round_T(s * w / sqrt(mean(s^2) + eps)),
 //   codes, scale_bytes = the 1 x 128 E4M3 quantisation of y as rounded to T,
 // so that the codes are those moe_quantize_fp8 gives for y. The norm reads s
-// before its rounding to T: one rounding per output. A row's sum of squares is
+// before its rounding to T. A row's sum of squares is
 // held in binary32; where the mean square overflows (|s| above about 1e17), or it and eps
 // nearly vanish (below 2^-100), it is taken again of s times a power of two (norm_of).
 //
@@ -89,10 +89,12 @@ struct Norm {
 
 // 1 / sqrt(ss / cols + eps) to about twice binary32's precision: an approximation and one Newton
 // step whose residual 1 - a inv^2 is formed by fused multiply-adds. With the product of a value
-// compensated too (finish_vector), the value is rounded once. Of 4096 x 5120 binary32 values 34 %
-// differ from the exact norm rounded once, against 51 % with three rounded products; of 29 million
-// bf16 values 223 do, nearly all by the rounding of s = x + r to binary32 where x and r are far apart.
-// (The sum of squares with its remainder carried along would leave 202, and takes 4 to 18 % longer.)
+// compensated too (finish_vector), what is rounded in front of the value itself is s and the sum of
+// squares, and a bf16 value goes through binary32. Rows whose sum is exact give binary32 values rounded
+// once; of 4096 x 5120 normal ones 34 % differ from the exact norm rounded once, by the sum's roundings,
+// against 51 % with three rounded products. Of 29 million bf16 values 223 differ, nearly all by the
+// rounding of s = x + r to binary32 where x and r are far apart. (The sum of squares with its remainder
+// carried along would leave 202, and takes 4 to 18 % longer.)
 __device__ __forceinline__ Norm inverse_rms(float ss, const NormArgs& n, float eps) {
   const float q = ss * n.inv_cols, q_lo = fmaf(-q, (float)n.cols, ss) * n.inv_cols;
   const float a = q + eps, z = a - q;
