@@ -168,7 +168,7 @@ typedef struct {
 
 /*
  * Workspace bytes needed by any entry point for this cfg and token count n
- * (moe_layer_decode's regions included, which are most of it at few tokens).
+ * (moe_layer_decode's included, which are most of it at few tokens).
  * The figure belongs to this version of the library: ask for it, keep none.
  * Returns MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED for a bad cfg.
  */

@@ -7,6 +7,7 @@ import torch
 
 import top_routing_expert_router_b200 as moe
 from synth import workloads as W
+from tests import moe_harness as H
 from tests.test_decode import Call
 
 CSRC = pathlib.Path(moe.__file__).parent / "csrc"
@@ -132,3 +133,56 @@ def test_abandoned_call_of_tokens_that_every_block_decides(name, n, monkeypatch)
     monkeypatch.delenv("MOE_TEST_STALL")
     c()
     assert moe.moe_sync_status(c.ws) == moe.MOE_OK and torch.equal(c.y, want.y)
+
+
+# ---- workspace ---------------------------------------------------------------------
+
+
+# Bytes for 1000 tokens before there was moe_layer_decode (and for fewer where they are the same still).
+FORMER = {
+    "tiny_f32": {1: 11264, 7: 35840, 64: 272128, 1000: 4166656},
+    "mixtral_8x7b": {1000: 91194368},
+    "deepseek_v3_small": {1000: 15774720},
+    "deepseek_v3_prefill": {1000: 285342720},
+    "deepseek_v3_decode_fp8_32e": {1: 8263424, 7: 10478336, 1000: 374758656},
+    "ragged_small": {1000: 3130112},
+}
+
+
+@pytest.mark.parametrize("name", FORMER)
+def test_a_batch_of_many_tokens_needs_no_more_for_the_decode_call(name):
+    cfg = H.cfg_for(W.get(name))
+    assert {n: moe.moe_workspace_size(cfg, n) for n in FORMER[name]} == FORMER[name]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["tiny_f32", "deepseek_v3_small", "deepseek_v3_decode_small_fp8"])
+def test_stages_find_nothing_in_the_workspace(name):
+    """moe_layer_decode writes where the other entry points have their scratch: between their calls it changes nothing."""
+    w = W.get(name, n=64)
+    dev = W.device_inputs(w)
+    c, n, act = Call(w, dev), w.n, dev["x"].dtype
+    c()
+    want_decode = c.y.clone()
+
+    def stages(between):
+        idx, tw = torch.empty(n, w.top_k, dtype=torch.int32, device="cuda"), torch.empty(n, w.top_k, device="cuda")
+        counts = torch.empty(w.n_routed, dtype=torch.int32, device="cuda")
+        offs = torch.empty(w.n_routed + 1, dtype=torch.int32, device="cuda")
+        perm, dest = (torch.empty(n * w.top_k, dtype=torch.int32, device="cuda") for _ in range(2))
+        xp, eo = (torch.zeros(n * w.top_k, w.d_model, dtype=act, device="cuda") for _ in range(2))
+        y = torch.empty(n, w.d_model, dtype=act, device="cuda")
+        moe.moe_route(c.cfg, n, dev["x"], c.weights, idx, tw, counts, None, c.ws)
+        between()
+        moe.moe_permute(c.cfg, n, dev["x"], idx, offs, perm, dest, xp, c.ws)
+        between()
+        moe.moe_expert_ffn(c.cfg, n, xp, offs, c.weights, eo, c.ws)
+        between()
+        moe.moe_combine(c.cfg, n, eo, dest, tw, dev["x"], c.weights, y, c.ws)
+        between()
+        return idx, tw, counts, offs, dest, eo, y
+
+    want = stages(lambda: None)
+    got = stages(c)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert torch.equal(c.y, want_decode) and moe.moe_sync_status(c.ws) == moe.MOE_OK

@@ -22,7 +22,9 @@ struct Plan {
   size_t diag, logits, rq, rc, ranking, capg, blk, idx, w, counts, offsets, perm, dest, xperm, h, eo, shh, sh, shoff, sched;
   size_t xq, sfx, hq, sfh, xsq, sfxs, hsq, sfhs;  // FP8 experts: E4M3 activations and their scale blocks
   size_t sfb, sfbs;  // FP8 SM-pair GEMMs: B scale blocks (routed, shared experts)
-  size_t dctr, dlog, dgu, deo, des, dhs, dhss, dxs, dh, dhh;  // moe_layer_decode: counters, binary64 logits, binary32 parts and outputs, scale bytes, h in two bf16 rows
+  // moe_layer_decode: counters, experts and gates, binary64 logits, binary32 parts and outputs, and x and h as they
+  // enter the experts (FP8: codes and scale bytes; bf16: h in two rows)
+  size_t dctr, didx, dw, dlog, dgu, deo, des, dxq, dxs, dh, dhs, dhh, dhss;
   size_t ep_off;  // expert parallelism: receive offsets of the rank's own experts
   size_t total;
   bool batched;   // the two-kernel router queues its undecided tokens for launch_refine (rq, rc reserved)
@@ -144,22 +146,30 @@ Plan make_plan(const moe_config& c, int64_t n, int32_t ep_world = 0, int64_t ep_
   p.sfb = take(fp8 ? sfb_bytes(fg, I, d) : 0);
   p.sfbs = take(fp8 && Is > 0 ? sfb_bytes(1, Is, d) : 0);
   p.ep_off = take(ep ? (size_t)(fg + 1) * 4 : 0);
-  // for moe_layer_decode of at most n tokens, whose needs grow with its tokens (decode_rows)
+  p.total = off;
+  // moe_layer_decode of at most n tokens, whose needs grow with its tokens (decode_rows). No call finds anything in the
+  // workspace but the status word, so its regions lie over the others': only batches of few tokens need more for it.
   const int64_t few = ep || c.cap_policy != MOE_CAP_NONE ? 0 : n < MOE_DECODE_MAX_TOKENS ? n : MOE_DECODE_MAX_TOKENS;
   if (few > 0) {
     const DecodeRows rows = decode_rows(few, c.d_model, c.n_routed, c.top_k, c.moe_intermediate_size, (int32_t)Is, c.dtype);
+    const int64_t slots = few * c.top_k;
+    const int64_t hb = fp8 ? 1 : 4;  // bytes of a value of h: a code, binary32, or two bf16
+    off = p.logits;                  // behind the status word
     p.dctr = take((size_t)decode_counters(c.d_model, c.n_routed, c.moe_intermediate_size, (int32_t)Is) * 4);
+    p.didx = take((size_t)slots * 4);
+    p.dw = take((size_t)slots * 4);
     p.dlog = take((size_t)few * c.n_routed * 8);
     p.dgu = take((size_t)2 * (rows.gu * I + rows.gus * Is) * 4);
     p.deo = take((size_t)rows.eo * d * 4);
     p.des = take((size_t)rows.es * d * 4);
+    p.dxq = take(fp8 ? (size_t)few * d : 0);
     p.dxs = take(fp8 ? (size_t)few * (d / 128) : 0);
-    p.dhs = take(fp8 ? (size_t)few * c.top_k * (I / 128) : 0);
+    p.dh = take((size_t)slots * I * hb);
+    p.dhs = take(fp8 ? (size_t)slots * (I / 128) : 0);
+    p.dhh = take((size_t)few * Is * hb);
     p.dhss = take(fp8 ? (size_t)few * (Is / 128) : 0);
-    p.dh = take(c.dtype == MOE_BF16 ? (size_t)2 * few * c.top_k * I * 2 : 0);
-    p.dhh = take(c.dtype == MOE_BF16 ? (size_t)2 * few * Is * 2 : 0);
+    if (off > p.total) p.total = off;
   }
-  p.total = off;
   return p;
 }
 
@@ -1014,14 +1024,14 @@ moe_status moe_layer_decode(const moe_config* cfg, int64_t n, const void* x, con
   a.ss_up = weights->ws_up_scale;
   a.ss_down = weights->ws_down_scale;
   a.quantize = fp8 && !given;
-  a.xq = given ? const_cast<uint8_t*>(x_codes_opt) : c.at<uint8_t>(c.p.xq);
+  a.xq = given ? const_cast<uint8_t*>(x_codes_opt) : c.at<uint8_t>(c.p.dxq);
   a.xs = given ? const_cast<uint8_t*>(x_scale_bytes_opt) : c.at<uint8_t>(c.p.dxs);
   a.cut = decode_splits(n, a.d, a.E, a.k, a.I, a.Is, a.dtype);
   a.logits = c.at<double>(c.p.dlog);
-  a.topk_idx = topk_idx_opt ? topk_idx_opt : c.at<int32_t>(c.p.idx);
-  a.topk_w = topk_w_opt ? topk_w_opt : c.at<float>(c.p.w);
-  a.h = c.at<void>(fp8 ? c.p.hq : f.dtype == MOE_BF16 ? c.p.dh : c.p.h);
-  a.hs = c.at<void>(fp8 ? c.p.hsq : f.dtype == MOE_BF16 ? c.p.dhh : c.p.shh);
+  a.topk_idx = topk_idx_opt ? topk_idx_opt : c.at<int32_t>(c.p.didx);
+  a.topk_w = topk_w_opt ? topk_w_opt : c.at<float>(c.p.dw);
+  a.h = c.at<void>(c.p.dh);
+  a.hs = c.at<void>(c.p.dhh);
   a.h_scale = c.at<uint8_t>(c.p.dhs);
   a.hs_scale = c.at<uint8_t>(c.p.dhss);
   a.gu = c.at<float>(c.p.dgu);
