@@ -80,8 +80,8 @@
  *     results are identical up to floating-point summation order.
  *     MOE_EP_TIMEOUT_MS bounds the expert-parallel barrier wait (see below).
  *     MOE_TEST_STALL=1 withholds one pipeline stage of the bf16 expert GEMM, and
- *     in moe_layer_decode the word that an expert's hidden rows are finished (2:
- *     that a token is decided), so that a bounded wait runs out and
+ *     in moe_layer_decode the counts of experts' finished hidden rows (2: of
+ *     decided tokens), so that a bounded wait runs out and
  *     MOE_ERR_TIMEOUT is reported (a test of the failure path; never set it
  *     otherwise).
  *     MOE_TEST_NO_TENSOR_MAPS=1 makes the bf16 tensor-core GEMMs report every

@@ -4,6 +4,8 @@
 //   logit[t, e] = x_t . W_r[e]
 // Reads W_r once per 16 tokens and x once per pair of experts; at one token it is bound by latency
 // (one round of loads), at 64 by the binary64 products (117 million at E = 256, d = 7168).
+#include <limits.h>
+
 #include "decode.cuh"
 
 namespace moe {
@@ -159,6 +161,13 @@ __global__ void __launch_bounds__(32 * kWarps) decode_router_kernel(DecodeArgs a
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i < a.ctr_bytes / 16; i += 32 * kWarps) reinterpret_cast<uint4*>(a.ctr)[i] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) a.status->status = MOE_OK;
+    if (a.test_stall) {  // counts that never reach what is waited for
+      __syncthreads();
+      if (a.test_stall == 1)
+        for (int e = threadIdx.x; e <= a.E; e += 32 * kWarps) a.ctr[kCtrExpert + e] = INT_MIN;
+      else if (threadIdx.x == 0)
+        a.ctr[kCtrTokenDone] = INT_MIN;
+    }
   }
   const int u = blockIdx.x;
   if (u < quants) {

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_simt_kernel(const __grid_c
   } else {
     for (int t; (t = claim(kCtrToken)) < a.n;) {
       decide_token(a, t, bias, &sm.decide, tid, sync, a.topk_idx + t * a.k, a.topk_w + t * a.k);
-      if (a.test_stall != 2 || t != 0) finish(a.ctr + kCtrTokenDone);
+      finish(a.ctr + kCtrTokenDone);
     }
     if (!wait(a.ctr + kCtrTokenDone, a.n)) return;
   }
@@ -273,9 +273,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_simt_kernel(const __grid_c
         run(Sums<8>{});
     }
     int32_t* done = a.ctr + kCtrExpert + (tl.down ? a.E + 1 + tl.r0 / kColumns : tl.e);
-    const bool withheld = a.test_stall == 1 && !tl.down && tl.r0 == 0;
     // the last expert's tile of these columns adds them up, the slots in order, the shared experts last
-    if (!withheld && finish(done) + 1 == sm.plan.n_act + shared && tl.down) {
+    if (finish(done) + 1 == sm.plan.n_act + shared && tl.down) {
       for (int i = tid; i < a.n * kColumns; i += kThreads) {
         const int t2 = i / kColumns, c = tl.r0 + i % kColumns;
         if (c >= a.d) continue;

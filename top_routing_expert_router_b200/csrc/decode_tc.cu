@@ -518,8 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         const int t = ctl->ticket;
         if (t >= a.n) break;
         decide_token(a, t, bias, &ctl->decide, tid, sync, a.topk_idx + t * a.k, a.topk_w + t * a.k);
-        // (decide_token ends with a barrier)
-        if (tid == 0 && (a.test_stall != 2 || t != 0)) add_release(a.ctr + kCtrTokenDone, 1);
+        if (tid == 0) add_release(a.ctr + kCtrTokenDone, 1);  // decide_token ends with a barrier
       }
       if (tid == 0) {
         ctl->routed = wait_counter(a.ctr + kCtrTokenDone, a.n, a.ctr, a.status, a.wait_cycles);
@@ -685,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
               }
             }
             if (tl.parts == 1) release();
-            if (a.test_stall != 1 || tl.r0 != 0) count(a.ctr + kCtrExpert + tl.e, INT_MAX);
+            count(a.ctr + kCtrExpert + tl.e, INT_MAX);
             continue;
           }
           {

@@ -217,7 +217,7 @@ struct DecodeArgs {
   moe_diag* diag;            // or nullptr
   int32_t* ctr;              // counters, zeroed (and the status word) by the first launch
   int32_t ctr_bytes;         // a multiple of 16
-  int32_t test_stall;        // fault injection: 1 = an expert's first gate/up tile is never reported finished, 2 = nor is a decision
+  int32_t test_stall;        // fault injection: 1 = no expert's gate/up tiles count as finished, 2 = no decision does
   int64_t wait_cycles;       // limit of any single wait, in SM clocks
   moe_diag* status;
 };
